@@ -83,6 +83,13 @@ SIGNATURES = {
     "vq_q4_0_rotate_h32": (_I, [_P, _P, _I64, _I64, _P, _P, _P]),
     "vq_greedy_workspace_bytes": (_SZ, [_I64, _I64]),
     "vq_hbm_read_probe": (_I, [_P, _SZ, _I, _I, _I, _I, _I, _P, _P]),
+    "vq_tree_attention": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64,
+                               _I64, _I64, _I64, _I64, _F, _P, _SZ, _P]),
+    "vq_tree_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "vq_tree_verify": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "vq_tree_verify_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "vq_kv_append": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                          _I64, _I64, _P]),
     "vq_status_string": (ctypes.c_char_p, [_I]),
     "vq_version": (_I, []),
 }
@@ -672,3 +679,199 @@ def hbm_read_probe(buf, sink, *, mode: str = "blocks", groups: int = 0, waves_pe
                                  _dev_ptr(sink, "sink"),
                                  _stream(stream))
     _check(st, "vq_hbm_read_probe")
+
+
+# ---------------------------------------------------------------- the rest of a speculative step
+
+def _stream_workspace(name: str, workspace, need: int, device, stream_handle: int):
+    """The Workspace of a call that always needs one: the caller's, or ("auto")
+    one cached per operator, device and stream, grown to `need` bytes."""
+    if isinstance(workspace, Workspace):
+        ws = workspace
+    elif workspace == "auto":
+        key = (name, device, stream_handle)
+        ws = _auto_ws.get(key)
+        if ws is None or ws.nbytes < need:
+            with _auto_lock:
+                ws = _auto_ws.get(key)
+                if ws is None or ws.nbytes < need:
+                    ws = Workspace(need, device)
+                    _auto_ws[key] = ws
+    else:
+        raise TypeError("workspace must be a Workspace or 'auto'")
+    ws.used_on(stream_handle)
+    return ws
+
+
+def _rows(t, name: str, lead, heads: int, dim: int) -> int:
+    """Row stride of a tensor [*lead][heads][dim] whose rows (heads * dim
+    contiguous elements) are all the same stride apart, as the slices of a
+    fused projection's output are."""
+    if tuple(t.shape) != (*lead, heads, dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (*lead, heads, dim)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    st = t.stride()
+    if (dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim):
+        raise ValueError("%s: the heads and channels of a row must be contiguous" % name)
+    row, count = None, 1
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
+        if size > 1:
+            if row is None:
+                if stride % count:
+                    raise ValueError("%s: rows must be evenly spaced" % name)
+                row = stride // count
+            elif stride != row * count:
+                raise ValueError("%s: rows must be evenly spaced" % name)
+        count *= size
+    return heads * dim if row is None else row
+
+
+def _ints(t, name: str, shape, dtype=None):
+    """Device pointer of an optional integer array (None: NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != (dtype or _torch().int32):
+        raise TypeError("%s must be %s" % (name, dtype or _torch().int32))
+    return _dev_ptr(t, name)
+
+
+def _cache(k_cache, v_cache, lead, dtype):
+    """(n_pages, kv_heads, page_size, head_dim) of a pair of caches with leading dimensions `lead`."""
+    at = len(lead)
+    if k_cache.dim() != at + 4 or tuple(k_cache.shape[:at]) != lead:
+        raise ValueError("k_cache must be [%sn_pages][kv_heads][page_size][head_dim]" % ("n_layers][" if at else ""))
+    n_pages, heads, page, dim = k_cache.shape[at:]
+    if tuple(v_cache.shape) != (*lead, n_pages, heads, page // 32, dim, 32):
+        raise ValueError("v_cache has shape %s, expected %s" %
+                         (tuple(v_cache.shape), (*lead, n_pages, heads, page // 32, dim, 32)))
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("the caches must have the dtype of the rows, %s" % dtype)
+    return n_pages, heads, page, dim
+
+
+def tree_attention(q, k, v, k_cache, v_cache, page_table, ctx_len, *, tree_mask=None, n_nodes=None, scale=None,
+                   out=None, workspace="auto", stream=None):
+    """Attention of each node of a drafted tree over its sequence's cached
+    tokens and the nodes it may see.
+
+    q: float16 / bfloat16 [B][n][Hq][D]; k, v: [B][n][H][D], the nodes' own
+    keys and values (all three may be slices of one fused projection);
+    k_cache: [P][H][page][D]; v_cache: [P][H][page/32][D][32]; page_table:
+    int32 [B][max_pages]; ctx_len: int32 [B].  tree_mask: int64 [B][n], bit j of
+    entry i set where node i sees node j (None: a chain, j <= i); n_nodes:
+    int32 [B] (None: n).  scale: 1 / sqrt(D) unless given.  Returns out
+    [B][n][Hq][D], zeros for nodes that see nothing and rows past n_nodes.
+    workspace: "auto" (a cached one per device and stream) or a Workspace."""
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [batch][n][q_heads][head_dim]")
+    B, n, Hq, D = q.shape
+    P, H, page, dim = _cache(k_cache, v_cache, (), q.dtype)
+    if dim != D:
+        raise ValueError("q has head_dim %d, the cache %d" % (D, dim))
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    qs, ks, vs = _rows(q, "q", (B, n), Hq, D), _rows(k, "k", (B, n), H, D), _rows(v, "v", (B, n), H, D)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch][max_pages]")
+    W = page_table.shape[1]
+    if out is None:
+        out = torch.empty((B, n, Hq, D), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (B, n, Hq, D) or out.dtype != q.dtype:
+        raise ValueError("out must be %s %s" % (q.dtype, (B, n, Hq, D)))
+    L = lib()
+    sh = _stream(stream)
+    ws = _stream_workspace("tree_attention", workspace,
+                           L.vq_tree_attention_workspace_bytes(B, n, Hq, H, D), q.device, sh)
+    st = L.vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
+                             _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+                             _ints(page_table, "page_table", (B, W)), _ints(ctx_len, "ctx_len", (B,)),
+                             _ints(tree_mask, "tree_mask", (B, n), torch.int64), _ints(n_nodes, "n_nodes", (B,)),
+                             _dev_ptr(out, "out"), B, n, Hq, H, D, page, P, W,
+                             D ** -0.5 if scale is None else float(scale), ws.ptr(), ws.nbytes, sh)
+    _check(st, "vq_tree_attention")
+    return out
+
+
+def tree_attention_workspace_bytes(batch: int, n: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of tree_attention (0 if the sizes are outside its limits)."""
+    return int(lib().vq_tree_attention_workspace_bytes(batch, n, q_heads, kv_heads, head_dim))
+
+
+def tree_verify_workspace_bytes(batch: int, n: int, vocab: int) -> int:
+    """Workspace bytes of tree_verify (0 if the sizes are outside its limits)."""
+    return int(lib().vq_tree_verify_workspace_bytes(batch, n, vocab))
+
+
+def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_nodes=None, temperature=None,
+                tokens_out=None, path_out=None, count_out=None, workspace="auto", stream=None):
+    """Acceptance of a drafted tree by the target's probabilities, from given
+    random numbers.
+
+    target: float32 / float16 / bfloat16 logits [B][n][V]; draft: the logits of
+    the same type that each node's children were drawn from, or None where
+    children were given rather than drawn; node_tokens: int32 [B][n];
+    uniforms: float32 [B][n] in [0, 1); noise: float32 [B][V] exponential
+    variates; parents: int32 [B][n] (None: a chain); n_nodes: int32 [B] (None:
+    n); temperature: float32 [B] (None: 1; 0: greedy).  Returns (tokens
+    int32 [B][n], path int32 [B][n], count int32 [B]): the committed tokens,
+    the nodes they follow, and how many there are."""
+    torch = _torch()
+    if target.dim() != 3:
+        raise ValueError("target must be [batch][n][vocab]")
+    B, n, V = target.shape
+    if draft is not None and (tuple(draft.shape) != (B, n, V) or draft.dtype != target.dtype):
+        raise ValueError("draft must have the target's shape and dtype")
+    if tokens_out is None:
+        tokens_out = torch.empty((B, n), dtype=torch.int32, device=target.device)
+    if path_out is None:
+        path_out = torch.empty((B, n), dtype=torch.int32, device=target.device)
+    if count_out is None:
+        count_out = torch.empty((B,), dtype=torch.int32, device=target.device)
+    L = lib()
+    sh = _stream(stream)
+    ws = _stream_workspace("tree_verify", workspace, L.vq_tree_verify_workspace_bytes(B, n, V), target.device, sh)
+    f32 = torch.float32
+    st = L.vq_tree_verify(_dev_ptr(target, "target"), None if draft is None else _dev_ptr(draft, "draft"),
+                          _dtype_code(target), _ints(node_tokens, "node_tokens", (B, n)),
+                          _ints(parents, "parents", (B, n)), _ints(n_nodes, "n_nodes", (B,)),
+                          _ints(temperature, "temperature", (B,), f32), _ints(uniforms, "uniforms", (B, n), f32),
+                          _ints(noise, "noise", (B, V), f32), _ints(tokens_out, "tokens_out", (B, n)),
+                          _ints(path_out, "path_out", (B, n)), _ints(count_out, "count_out", (B,)), B, n, V,
+                          ws.ptr(), ws.nbytes, sh)
+    _check(st, "vq_tree_verify")
+    return tokens_out, path_out, count_out
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=None, len_out=None, stream=None):
+    """Writes rows of keys and values into the cache: position ctx_len[b] + i
+    takes row path[b][i] for i < count[b] (None: row i; all n rows).
+
+    k, v: float16 / bfloat16 [B][n][H][D] with caches as for tree_attention, or
+    [L][B][n][H][D] with caches [L][P]... of L layers; path: int32 [B][n];
+    count: int32 [B], as tree_verify returns them.  Returns the new lengths,
+    int32 [B]."""
+    torch = _torch()
+    if k.dim() not in (4, 5):
+        raise ValueError("k must be [n_layers][batch][n][kv_heads][head_dim] or without the layers")
+    lead = tuple(k.shape[:-4])
+    B, n, H, D = k.shape[-4:]
+    P, heads, page, dim = _cache(k_cache, v_cache, lead, k.dtype)
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must have one dtype")
+    ks, vs = _rows(k, "k", (*lead, B, n), heads, dim), _rows(v, "v", (*lead, B, n), heads, dim)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch][max_pages]")
+    W = page_table.shape[1]
+    if len_out is None:
+        len_out = torch.empty((B,), dtype=torch.int32, device=k.device)
+    st = lib().vq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _dev_ptr(k_cache, "k_cache"),
+                            _dev_ptr(v_cache, "v_cache"), _ints(page_table, "page_table", (B, W)),
+                            _ints(ctx_len, "ctx_len", (B,)), _ints(path, "path", (B, n)),
+                            _ints(count, "count", (B,)), _ints(len_out, "len_out", (B,)),
+                            lead[0] if lead else 1, B, n, heads, dim, page, P, W, _stream(stream))
+    _check(st, "vq_kv_append")
+    return len_out

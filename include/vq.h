@@ -472,6 +472,155 @@ int vq_greedy_verify(const void *logits, int logits_dtype, int64_t n_rows, int64
 size_t vq_greedy_workspace_bytes(int64_t n_rows, int64_t vocab);
 
 /*
+ * The rest of a speculative step -- the operations between the verify GEMMs
+ * and around them, for a batch of sequences that each check a tree of drafted
+ * tokens ([P1] "A block-diffusion drafter, verified exactly": one batched
+ * target forward checks the whole draft block).
+ *
+ * The tree of a sequence has up to VQ_MAX_TREE_NODES nodes.  Node 0 is the
+ * last committed token (its keys and values are computed by this step too),
+ * node i >= 1 a drafted token; a parent comes before its children.  A chain
+ * (node i hangs on node i - 1) is the draft block of vq_greedy_verify.
+ *
+ * The cache of a layer holds the keys and values of committed tokens in
+ * pages of page_size tokens (32, 64, 128 or 256):
+ *   k_cache  [n_pages][kv_heads][page_size][head_dim]
+ *   v_cache  [n_pages][kv_heads][page_size / 32][head_dim][32]: every 32
+ *            tokens of a head are stored transposed, so that 8 consecutive
+ *            tokens of one channel are the 16 bytes a lane feeds to the
+ *            matrix instruction that multiplies probabilities and values.
+ *   page_table int32 [batch][max_pages]: token t of sequence b is in page
+ *            page_table[b][t / page_size] at t % page_size.  Entries past a
+ *            sequence's tokens are not read; an entry outside [0, n_pages)
+ *            reads as zeros and drops what is written.
+ *   ctx_len  int32 [batch]: committed tokens in the cache (taken as 0 where
+ *            negative and as max_pages * page_size where larger).
+ * The drafted tokens' keys and values are not in the cache: they are the rows
+ * of the step's own projections, and vq_kv_append writes those of the
+ * accepted path into the cache once the step is verified.
+ *
+ * Shared limits: 1 <= batch <= VQ_MAX_BATCH, 1 <= q_heads, kv_heads <=
+ * VQ_MAX_HEADS, q_heads % kv_heads == 0, head_dim 64, 128 or 256, 1 <= n_pages
+ * <= VQ_MAX_DIM, 1 <= max_pages, max_pages * page_size <= 2^30.  Row strides
+ * are in elements, multiples of 8, at least the row's width and at most
+ * VQ_MAX_DIM: the rows of q, k and v may be slices of one fused projection.
+ */
+#define VQ_MAX_TREE_NODES 64
+#define VQ_MAX_BATCH 4096
+#define VQ_MAX_HEADS 1024
+
+/*
+ * vq_tree_attention -- attention of every node over its sequence's cache and
+ * the nodes it may see.  Query head h reads key/value head h / (q_heads /
+ * kv_heads).  For node i of sequence b, with N = n_nodes[b] (n where n_nodes
+ * is NULL) taken into [0, n]:
+ *   visible = cache positions t < ctx_len[b], and the nodes j < N with bit j
+ *             of tree_mask[b][i] set (tree_mask NULL: j <= i, a chain)
+ *   s = scale * (q . k),  out = sum exp(s - max s) v / sum exp(s - max s)
+ * over the visible ones.  A node that sees nothing, and every row i >= N,
+ * gets zeros.  What a node does not see never reaches its output, infinities
+ * and NaN included.
+ *   dtype     F16 or BF16, of q, k, v, the caches and out.
+ *   q         [batch * n] rows of q_heads * head_dim, q_stride apart
+ *   k, v      [batch * n] rows of kv_heads * head_dim, k_stride, v_stride
+ *             apart: the nodes' own keys and values
+ *   tree_mask uint64 [batch][n] or NULL; n_nodes int32 [batch] or NULL
+ *   out       [batch][n][q_heads][head_dim]
+ *   workspace vq_tree_attention_workspace_bytes() bytes, any contents
+ *             (VQ_ERR_WORKSPACE if NULL or smaller); calls that share one must
+ *             not overlap in time.
+ * Scores, softmax statistics and sums are fp32; the probabilities are rounded
+ * to dtype for the product with the values.  Results are the same bits from
+ * run to run; where a long context is cut between workgroups follows the
+ * whole call (all sequences' lengths) and the device's CU count.
+ */
+int vq_tree_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, int dtype,
+                      const void *k_cache, const void *v_cache,
+                      const int32_t *page_table, const int32_t *ctx_len,
+                      const uint64_t *tree_mask, const int32_t *n_nodes, void *out,
+                      int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                      int64_t page_size, int64_t n_pages, int64_t max_pages, float scale,
+                      void *workspace, size_t workspace_bytes, void *stream);
+/* 0 for sizes outside the limits. */
+size_t vq_tree_attention_workspace_bytes(int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads,
+                                         int64_t head_dim);
+
+/*
+ * vq_tree_verify -- acceptance of a drafted tree when the output has to follow
+ * the target's distribution (vq_greedy_verify keeps the target's greedy
+ * choices).  Random numbers are inputs, so the result is a function of the
+ * arguments alone.  At a node v, with p = softmax(target[v] / T):
+ *   its children c_0, c_1, ... (in node order) are tried in turn.  With draft
+ *   logits, each was drawn from q = softmax(draft[v] / T):
+ *     r_j(x) = max(0, p(x) - S_j q(x)), s_j = sum_x r_j(x),
+ *     S_0 = 0, s_0 = 1, S_(j+1) = S_j + s_j
+ *     child c_j with token x is accepted iff  u[c_j] q(x) s_j < r_j(x)
+ *   (each rejection replaces p by the normalised positive part of p - q; the
+ *   nested differences collapse to one scalar S).  Without draft logits each
+ *   child was given, not drawn (q is 1 at its token): r_(j+1) is r_j with
+ *   that token set to 0, s_(j+1) = s_j - r_j(x), and c_j is accepted iff
+ *   u[c_j] s_j < r_j(x).
+ *   An accepted child becomes the next v.  When no child is accepted the step
+ *   ends with the token argmax_x r(x) / noise[x] over r(x) > 0, which is
+ *   distributed as r / sum r when noise holds independent exponential
+ *   variates; the lowest index wins ties, and p stands in for an r that is
+ *   zero everywhere (and token 0 where p has no positive entry).
+ *   T = 0: a child is accepted iff its token is the target's greedy choice
+ *   (argmax as in vq_greedy_verify), and the last token is that choice.
+ * Softmax terms and sums are fp32.  A logit of -inf has probability 0; other
+ * logits are finite, and NaN only where T = 0.
+ *   target    [batch][n][vocab], logits_dtype F32, F16 or BF16
+ *   draft     [batch][n][vocab] of the same type, or NULL; row v is read only
+ *             if node v has children
+ *   node_tokens int32 [batch][n]: the drafted token of each node (entry 0 is
+ *             not read); a token outside [0, vocab) is never accepted
+ *   parents   int32 [batch][n] or NULL (chain); a node i >= 1 whose parent is
+ *             not in [0, i) is no node's child
+ *   n_nodes   int32 [batch] or NULL (n), taken into [0, n]; 0 gives count 0
+ *   temperature fp32 [batch] or NULL (1), >= 0
+ *   uniforms  fp32 [batch][n] in [0, 1)
+ *   noise     fp32 [batch][vocab], > 0
+ *   count_out int32 [batch]: a + 1 for a accepted nodes
+ *   path_out  int32 [batch][n]: node 0, then the accepted nodes; -1 from count on
+ *   tokens_out int32 [batch][n]: the committed tokens, tokens_out[b][k] follows
+ *             node path_out[b][k]; -1 from count on
+ *   workspace vq_tree_verify_workspace_bytes() bytes, any contents
+ *             (VQ_ERR_WORKSPACE if NULL or smaller).
+ * Sizes: 1 <= n <= VQ_MAX_TREE_NODES, 1 <= vocab <= VQ_MAX_DIM.
+ */
+int vq_tree_verify(const void *target, const void *draft, int logits_dtype,
+                   const int32_t *node_tokens, const int32_t *parents, const int32_t *n_nodes,
+                   const float *temperature, const float *uniforms, const float *noise,
+                   int32_t *tokens_out, int32_t *path_out, int32_t *count_out,
+                   int64_t batch, int64_t n, int64_t vocab,
+                   void *workspace, size_t workspace_bytes, void *stream);
+size_t vq_tree_verify_workspace_bytes(int64_t batch, int64_t n, int64_t vocab);
+
+/*
+ * vq_kv_append -- writes rows of keys and values into the pages of n_layers
+ * layers: position ctx_len[b] + i of sequence b takes row path[b][i] of its n
+ * rows, for i < count[b] (path NULL: row i; count NULL: all n).  With the path
+ * and count of vq_tree_verify this commits the accepted nodes; without, it
+ * fills the cache from a prompt's projections.  Positions from max_pages *
+ * page_size on and rows outside [0, n) are dropped.
+ *   k, v      [n_layers][batch * n] rows of kv_heads * head_dim, k_stride and
+ *             v_stride apart; dtype F16 or BF16
+ *   k_cache, v_cache  the layers' caches one after the other
+ *   path      int32 [batch][n] or NULL; count int32 [batch] or NULL, taken
+ *             into [0, n]
+ *   len_out   int32 [batch] or NULL: ctx_len[b] + count[b], at most max_pages *
+ *             page_size
+ * Every destination is written by one row only as long as no page belongs to
+ * two sequences.  Sizes: 1 <= n_layers <= VQ_MAX_HEADS, 1 <= n <= VQ_MAX_DIM.
+ */
+int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype,
+                 void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *ctx_len,
+                 const int32_t *path, const int32_t *count, int32_t *len_out,
+                 int64_t n_layers, int64_t batch, int64_t n, int64_t kv_heads, int64_t head_dim,
+                 int64_t page_size, int64_t n_pages, int64_t max_pages, void *stream);
+
+/*
  * vq_hbm_read_probe -- a plain read of `bytes` of device memory at `buf`,
  * the bandwidth the verify GEMM's weight stream is measured against ([P1]
  * TL;DR: decode streams the weights at a fraction of the card's bandwidth,
