@@ -683,12 +683,19 @@ def hbm_read_probe(buf, sink, *, mode: str = "blocks", groups: int = 0, waves_pe
 
 # ---------------------------------------------------------------- the rest of a speculative step
 
+def _raw_stream(stream) -> int:
+    """_stream for calls that take a few microseconds: torch's handle of the
+    current stream without making a Stream object (2.7 us) on the way."""
+    if stream is not None:
+        return _stream(stream)
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+
+
 def _stream_workspace(name: str, workspace, need: int, device, stream_handle: int):
     """The Workspace of a call that always needs one: the caller's, or ("auto")
     one cached per operator, device and stream, grown to `need` bytes."""
-    if isinstance(workspace, Workspace):
-        ws = workspace
-    elif workspace == "auto":
+    if workspace == "auto":
         key = (name, device, stream_handle)
         ws = _auto_ws.get(key)
         if ws is None or ws.nbytes < need:
@@ -697,54 +704,55 @@ def _stream_workspace(name: str, workspace, need: int, device, stream_handle: in
                 if ws is None or ws.nbytes < need:
                     ws = Workspace(need, device)
                     _auto_ws[key] = ws
+    elif isinstance(workspace, Workspace):
+        ws = workspace
     else:
         raise TypeError("workspace must be a Workspace or 'auto'")
     ws.used_on(stream_handle)
     return ws
 
 
-def _rows(t, name: str, lead, heads: int, dim: int) -> int:
-    """Row stride of a tensor [*lead][heads][dim] whose rows (heads * dim
+def _rows(t, name: str, shape) -> int:
+    """Row stride of a tensor [...][heads][dim] whose rows (heads * dim
     contiguous elements) are all the same stride apart, as the slices of a
     fused projection's output are."""
-    if tuple(t.shape) != (*lead, heads, dim):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (*lead, heads, dim)))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     st = t.stride()
-    if (dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim):
+    heads, dim = shape[-2:]
+    if st[-1] != 1 or (heads > 1 and st[-2] != dim):
         raise ValueError("%s: the heads and channels of a row must be contiguous" % name)
-    row, count = None, 1
-    for size, stride in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
-        if size > 1:
-            if row is None:
-                if stride % count:
-                    raise ValueError("%s: rows must be evenly spaced" % name)
-                row = stride // count
-            elif stride != row * count:
+    row, rows = 0, 1
+    for at in range(len(shape) - 3, -1, -1):
+        if shape[at] > 1:
+            if row == 0:
+                row = st[at]  # every dimension inside this one has size 1
+            elif st[at] != row * rows:
                 raise ValueError("%s: rows must be evenly spaced" % name)
-        count *= size
-    return heads * dim if row is None else row
+            rows *= shape[at]
+    return row if rows > 1 else heads * dim
 
 
-def _ints(t, name: str, shape, dtype=None):
-    """Device pointer of an optional integer array (None: NULL)."""
+def _array(t, name: str, shape, dtype):
+    """Device pointer of a contiguous array, or NULL for None."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    if t.dtype != (dtype or _torch().int32):
-        raise TypeError("%s must be %s" % (name, dtype or _torch().int32))
-    return _dev_ptr(t, name)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s" % (name, dtype, tuple(shape)))
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("%s must be a contiguous device tensor" % name)
+    return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, lead, dtype):
     """(n_pages, kv_heads, page_size, head_dim) of a pair of caches with leading dimensions `lead`."""
-    at = len(lead)
-    if k_cache.dim() != at + 4 or tuple(k_cache.shape[:at]) != lead:
-        raise ValueError("k_cache must be [%sn_pages][kv_heads][page_size][head_dim]" % ("n_layers][" if at else ""))
-    n_pages, heads, page, dim = k_cache.shape[at:]
-    if tuple(v_cache.shape) != (*lead, n_pages, heads, page // 32, dim, 32):
+    shape = k_cache.shape
+    if len(shape) != len(lead) + 4 or shape[:-4] != lead:
+        raise ValueError("k_cache must be [%sn_pages][kv_heads][page_size][head_dim]" % ("n_layers][" if lead else ""))
+    n_pages, heads, page, dim = shape[-4:]
+    if v_cache.shape != (*lead, n_pages, heads, page // 32, dim, 32):
         raise ValueError("v_cache has shape %s, expected %s" %
                          (tuple(v_cache.shape), (*lead, n_pages, heads, page // 32, dim, 32)))
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
@@ -768,30 +776,29 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, ctx_len, *, tree_mask=
     torch = _torch()
     if q.dim() != 4:
         raise ValueError("q must be [batch][n][q_heads][head_dim]")
-    B, n, Hq, D = q.shape
-    P, H, page, dim = _cache(k_cache, v_cache, (), q.dtype)
+    shape = B, n, Hq, D = tuple(q.shape)
+    dtype = q.dtype
+    P, H, page, dim = _cache(k_cache, v_cache, (), dtype)
     if dim != D:
         raise ValueError("q has head_dim %d, the cache %d" % (D, dim))
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    qs, ks, vs = _rows(q, "q", (B, n), Hq, D), _rows(k, "k", (B, n), H, D), _rows(v, "v", (B, n), H, D)
+    kv_shape = (B, n, H, D)
+    qs, ks, vs = _rows(q, "q", shape), _rows(k, "k", kv_shape), _rows(v, "v", kv_shape)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch][max_pages]")
     W = page_table.shape[1]
     if out is None:
-        out = torch.empty((B, n, Hq, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (B, n, Hq, D) or out.dtype != q.dtype:
-        raise ValueError("out must be %s %s" % (q.dtype, (B, n, Hq, D)))
-    L = lib()
-    sh = _stream(stream)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    L, sh, i32 = lib(), _raw_stream(stream), torch.int32
     ws = _stream_workspace("tree_attention", workspace,
                            L.vq_tree_attention_workspace_bytes(B, n, Hq, H, D), q.device, sh)
     st = L.vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
                              _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                             _ints(page_table, "page_table", (B, W)), _ints(ctx_len, "ctx_len", (B,)),
-                             _ints(tree_mask, "tree_mask", (B, n), torch.int64), _ints(n_nodes, "n_nodes", (B,)),
-                             _dev_ptr(out, "out"), B, n, Hq, H, D, page, P, W,
-                             D ** -0.5 if scale is None else float(scale), ws.ptr(), ws.nbytes, sh)
+                             _array(page_table, "page_table", (B, W), i32), _array(ctx_len, "ctx_len", (B,), i32),
+                             _array(tree_mask, "tree_mask", (B, n), torch.int64),
+                             _array(n_nodes, "n_nodes", (B,), i32), _array(out, "out", shape, dtype), B, n, Hq, H,
+                             D, page, P, W, D ** -0.5 if scale is None else scale, ws.ptr(), ws.nbytes, sh)
     _check(st, "vq_tree_attention")
     return out
 
@@ -822,26 +829,23 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
     torch = _torch()
     if target.dim() != 3:
         raise ValueError("target must be [batch][n][vocab]")
-    B, n, V = target.shape
-    if draft is not None and (tuple(draft.shape) != (B, n, V) or draft.dtype != target.dtype):
-        raise ValueError("draft must have the target's shape and dtype")
+    shape = B, n, V = tuple(target.shape)
+    i32, f32, dev = torch.int32, torch.float32, target.device
     if tokens_out is None:
-        tokens_out = torch.empty((B, n), dtype=torch.int32, device=target.device)
+        tokens_out = torch.empty((B, n), dtype=i32, device=dev)
     if path_out is None:
-        path_out = torch.empty((B, n), dtype=torch.int32, device=target.device)
+        path_out = torch.empty((B, n), dtype=i32, device=dev)
     if count_out is None:
-        count_out = torch.empty((B,), dtype=torch.int32, device=target.device)
-    L = lib()
-    sh = _stream(stream)
-    ws = _stream_workspace("tree_verify", workspace, L.vq_tree_verify_workspace_bytes(B, n, V), target.device, sh)
-    f32 = torch.float32
-    st = L.vq_tree_verify(_dev_ptr(target, "target"), None if draft is None else _dev_ptr(draft, "draft"),
-                          _dtype_code(target), _ints(node_tokens, "node_tokens", (B, n)),
-                          _ints(parents, "parents", (B, n)), _ints(n_nodes, "n_nodes", (B,)),
-                          _ints(temperature, "temperature", (B,), f32), _ints(uniforms, "uniforms", (B, n), f32),
-                          _ints(noise, "noise", (B, V), f32), _ints(tokens_out, "tokens_out", (B, n)),
-                          _ints(path_out, "path_out", (B, n)), _ints(count_out, "count_out", (B,)), B, n, V,
-                          ws.ptr(), ws.nbytes, sh)
+        count_out = torch.empty((B,), dtype=i32, device=dev)
+    L, sh = lib(), _raw_stream(stream)
+    ws = _stream_workspace("tree_verify", workspace, L.vq_tree_verify_workspace_bytes(B, n, V), dev, sh)
+    st = L.vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
+                          _dtype_code(target), _array(node_tokens, "node_tokens", (B, n), i32),
+                          _array(parents, "parents", (B, n), i32), _array(n_nodes, "n_nodes", (B,), i32),
+                          _array(temperature, "temperature", (B,), f32),
+                          _array(uniforms, "uniforms", (B, n), f32), _array(noise, "noise", (B, V), f32),
+                          _array(tokens_out, "tokens_out", (B, n), i32), _array(path_out, "path_out", (B, n), i32),
+                          _array(count_out, "count_out", (B,), i32), B, n, V, ws.ptr(), ws.nbytes, sh)
     _check(st, "vq_tree_verify")
     return tokens_out, path_out, count_out
 
@@ -857,21 +861,23 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
     torch = _torch()
     if k.dim() not in (4, 5):
         raise ValueError("k must be [n_layers][batch][n][kv_heads][head_dim] or without the layers")
-    lead = tuple(k.shape[:-4])
-    B, n, H, D = k.shape[-4:]
-    P, heads, page, dim = _cache(k_cache, v_cache, lead, k.dtype)
-    if v.dtype != k.dtype:
+    shape = tuple(k.shape)
+    lead, (B, n, H, D), dtype = shape[:-4], shape[-4:], k.dtype
+    P, heads, page, dim = _cache(k_cache, v_cache, lead, dtype)
+    if (heads, dim) != (H, D):
+        raise ValueError("the cache holds %d heads of %d, the rows %d of %d" % (heads, dim, H, D))
+    if v.dtype != dtype:
         raise TypeError("k and v must have one dtype")
-    ks, vs = _rows(k, "k", (*lead, B, n), heads, dim), _rows(v, "v", (*lead, B, n), heads, dim)
+    ks, vs = _rows(k, "k", shape), _rows(v, "v", shape)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [batch][max_pages]")
-    W = page_table.shape[1]
+    W, i32 = page_table.shape[1], torch.int32
     if len_out is None:
-        len_out = torch.empty((B,), dtype=torch.int32, device=k.device)
+        len_out = torch.empty((B,), dtype=i32, device=k.device)
     st = lib().vq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _dev_ptr(k_cache, "k_cache"),
-                            _dev_ptr(v_cache, "v_cache"), _ints(page_table, "page_table", (B, W)),
-                            _ints(ctx_len, "ctx_len", (B,)), _ints(path, "path", (B, n)),
-                            _ints(count, "count", (B,)), _ints(len_out, "len_out", (B,)),
-                            lead[0] if lead else 1, B, n, heads, dim, page, P, W, _stream(stream))
+                            _dev_ptr(v_cache, "v_cache"), _array(page_table, "page_table", (B, W), i32),
+                            _array(ctx_len, "ctx_len", (B,), i32), _array(path, "path", (B, n), i32),
+                            _array(count, "count", (B,), i32), _array(len_out, "len_out", (B,), i32),
+                            lead[0] if lead else 1, B, n, H, D, page, P, W, _raw_stream(stream))
     _check(st, "vq_kv_append")
     return len_out

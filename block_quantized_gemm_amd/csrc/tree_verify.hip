@@ -11,9 +11,13 @@
 // with probability r_x / sum r, so no running sum over the vocabulary is
 // compared with a threshold, and the result does not hang on its rounding.
 //
-// Two kernels: the first reads every row once for its maximum and sum of
-// exponentials, one workgroup per row; the second, one workgroup per
-// sequence, walks the tree and draws the last token.
+// Three kernels.  The first reads every row once, a wave per chunk of 2048
+// logits held in registers, and leaves each chunk's maximum and sum of
+// exponentials (or, for a greedy sequence, its best key).  The second, one
+// workgroup per sequence, joins the chunks, looks the drafted tokens up and
+// walks the tree; only a node that is tried again after a rejection costs it
+// another pass over that node's two rows.  The third draws the last token,
+// the row split over many workgroups; the last to arrive writes it.
 #include "tree_internal.h"
 #include "vq_device.h"
 
@@ -21,34 +25,34 @@ namespace vq {
 
 namespace {
 
-constexpr int kStatThreads = 256;
+constexpr int kNodes = VQ_MAX_TREE_NODES;
+constexpr int kThreads = 256;
 constexpr int kWalkThreads = 1024;
+constexpr int kPieces = 4;                   // pieces of 8 logits a lane holds
+constexpr int kChunk = 64 * 8 * kPieces;     // logits of a wave of the first kernel
+constexpr int kDrawChunk = kThreads * 8 * 2;  // tokens of a workgroup of the third
 
 struct KArgs {
     const void *target, *draft;
     const int32_t *node_tokens, *parents, *n_nodes;
     const float *temperature, *uniforms, *noise;
     int32_t *tokens_out, *path_out, *count_out;
-    int n, vocab;
+    uint2 *part;          // [batch][target, draft][n][chunks]
+    struct Last *last;    // [batch]
+    int n, vocab, chunks;
 };
 
-// What the first kernel leaves of a row: softmax maximum and 1 / sum, and the
-// greedy choice.
-struct RowStat {
-    float m, inv, mq, invq;
-    int32_t best;
-    int32_t pad[3];
+// What the walk leaves for the draw: the node whose row is drawn from, the
+// softmax terms of its rows, the remainder's scalar S, the rejected tokens
+// (without draft logits), and the draw's best key and arrivals.
+struct Last {
+    uint64_t key;
+    uint32_t arrived;
+    int32_t node, at;     // node < 0: no draw; at: the token's place in the outputs
+    float m, inv, mq, invq, S;
+    int32_t n_gone;
+    int32_t gone[kNodes];
 };
-
-template <int DT>
-__device__ __forceinline__ float logit_at(const void *p, int64_t i) {
-    if constexpr (DT == VQ_DTYPE_F32)
-        return static_cast<const float *>(p)[i];
-    else if constexpr (DT == VQ_DTYPE_BF16)
-        return __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
-    else
-        return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<const uint16_t *>(p)[i]));
-}
 
 // Order-preserving key of a float and its index: larger values first, NaN
 // before all, -0 as +0, the lower index of equal values.
@@ -74,23 +78,26 @@ __device__ __forceinline__ uint64_t lane_xor(uint64_t x, int off) {
     return ((uint64_t)hi << 32) | lo;
 }
 
-// Reduction over a workgroup of THREADS; every thread gets it.
-template <int THREADS, typename Op, typename T>
-__device__ __forceinline__ T block_reduce(T x, Op op, uint64_t *red64) {
-    T *red = reinterpret_cast<T *>(red64);
+template <typename Op, typename T>
+__device__ __forceinline__ T wave_reduce(T x, Op op) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
         x = op(x, lane_xor(x, off));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = red[0];
-#pragma unroll
-    for (int w = 1; w < THREADS / 64; ++w)
-        x = op(x, red[w]);
     return x;
 }
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const void *p, int64_t i) {
+    if constexpr (DT == VQ_DTYPE_F32)
+        return static_cast<const float *>(p)[i];
+    else if constexpr (DT == VQ_DTYPE_BF16)
+        return __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
+    else
+        return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<const uint16_t *>(p)[i]));
+}
+
+// max(0, p - S q): one rounding, the product's is inside the fma.
+__device__ __forceinline__ float left_of(float p, float S, float q) { return fmaxf(0.f, fmaf(-S, q, p)); }
 
 __device__ __forceinline__ int live_nodes(const KArgs &a, int b) {
     return a.n_nodes ? min(max(a.n_nodes[b], 0), a.n) : a.n;
@@ -105,116 +112,223 @@ __device__ __forceinline__ float exponent_scale(const KArgs &a, int b) {
     return t > 0.f ? 1.44269504088896f / t : 0.f;
 }
 
+// One row of logits, read 8 at a time from 16-byte aligned addresses: the row
+// begins `shift` elements after its first piece.  Elements outside the row
+// read as -inf; nothing past the row's last dword is touched.
 template <int DT>
-__device__ __forceinline__ void softmax_stats(const void *row, int vocab, float c, uint64_t *red, float &m,
-                                              float &inv) {
-    float mx = -INFINITY;
-    for (int x = (int)threadIdx.x; x < vocab; x += kStatThreads)
-        mx = fmaxf(mx, logit_at<DT>(row, x));
-    m = block_reduce<kStatThreads>(mx, MaxOp{}, red);
-    float sum = 0.f;
-    for (int x = (int)threadIdx.x; x < vocab; x += kStatThreads)
-        sum += exp2f((logit_at<DT>(row, x) - m) * c);
-    inv = 1.f / block_reduce<kStatThreads>(sum, SumOp{}, red);
-}
+struct Row {
+    static constexpr int kElem = DT == VQ_DTYPE_F32 ? 4 : 2;
+    rsrc_t r;
+    int shift, vocab;
+
+    __device__ __forceinline__ Row(const void *base, const KArgs &a, int b, int v) : vocab(a.vocab) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(base) + ((uint64_t)b * a.n + v) * (uint64_t)a.vocab * kElem;
+        shift = uniform((int)(at & 15) / kElem);
+        r = make_rsrc(reinterpret_cast<const void *>(at & ~(uintptr_t)15),
+                      (uint32_t)((shift + a.vocab) * kElem + 3) & ~3u);
+    }
+    static __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+    // elements pos - shift .. + 8 of the row, pos a multiple of 8
+    __device__ __forceinline__ void load(int pos, u32x4 (&raw)[kElem / 2]) const {
+#pragma unroll
+        for (int i = 0; i < kElem / 2; ++i)
+            raw[i] = bload16<kAuxCached>(r, pos * kElem + 16 * i, 0);
+    }
+    __device__ __forceinline__ void values(const u32x4 (&raw)[kElem / 2], int pos, float (&x)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == VQ_DTYPE_F32) {
+                const uint32_t w = raw[e >> 2][e & 3];
+                x[e] = __builtin_bit_cast(float, w);
+            } else {
+                const uint32_t w = raw[0][e >> 1], h = e & 1 ? w >> 16 : w & 0xFFFFu;
+                x[e] = DT == VQ_DTYPE_BF16 ? __builtin_bit_cast(float, h << 16) : h2f(h);
+            }
+        }
+        if (pos < shift || pos + 8 > shift + vocab)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = pos + e >= shift && pos + e < shift + vocab ? x[e] : -INFINITY;
+    }
+    __device__ __forceinline__ int end() const { return shift + vocab; }
+};
 
 template <int DT>
-__device__ __forceinline__ const void *row_ptr(const void *base, const KArgs &a, int b, int v) {
-    constexpr int kElem = DT == VQ_DTYPE_F32 ? 4 : 2;
-    return static_cast<const char *>(base) + ((int64_t)b * a.n + v) * a.vocab * kElem;
-}
-
-template <int DT>
-__global__ __launch_bounds__(kStatThreads) void tree_row_stats(KArgs a, RowStat *stats) {
-    __shared__ uint64_t red[kStatThreads / 64];
-    const int v = (int)blockIdx.x, b = (int)blockIdx.y, nodes = live_nodes(a, b);
-    if (v >= nodes)
+__global__ __launch_bounds__(kThreads) void tree_row_stats(KArgs a) {
+    const int lane = (int)(threadIdx.x & 63), chunk = (int)blockIdx.x * (kThreads / 64) + wave_id();
+    const bool draft = (int)blockIdx.y >= a.n;
+    const int v = (int)blockIdx.y - (draft ? a.n : 0), b = (int)blockIdx.z, nodes = live_nodes(a, b);
+    if (v >= nodes || chunk >= a.chunks)
         return;
     const float c = exponent_scale(a, b);
-    RowStat st{};
-    const void *row = row_ptr<DT>(a.target, a, b, v);
+    if (draft) {
+        // a drafter's row counts only where it has children and is asked for probabilities
+        if (c == 0.f || !__any(lane > v && lane < nodes && parent_of(a, b, lane) == v))
+            return;
+    }
+    const Row<DT> row(draft ? a.draft : a.target, a, b, v);
+    u32x4 raw[kPieces][Row<DT>::kElem / 2];
+    const int pos0 = chunk * kChunk + lane * 8;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+        row.load(pos0 + i * 512, raw[i]);
+    uint2 *out = a.part + (((int64_t)b * 2 + (draft ? 1 : 0)) * a.n + v) * a.chunks + chunk;
+    float x[8];
     if (c == 0.f) {
         uint64_t best = 0;
-        for (int x = (int)threadIdx.x; x < a.vocab; x += kStatThreads) {
-            const uint64_t k = key_of(logit_at<DT>(row, x), x);
-            best = k > best ? k : best;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int pos = pos0 + i * 512;
+            row.values(raw[i], pos, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint64_t k = key_of(x[e], pos + e - row.shift);
+                if (pos + e >= row.shift && pos + e < row.end())
+                    best = k > best ? k : best;
+            }
         }
-        st.best = (int32_t)~(uint32_t)block_reduce<kStatThreads>(best, MaxOp{}, red);
-    } else {
-        softmax_stats<DT>(row, a.vocab, c, red, st.m, st.inv);
-        bool inner = false;
-        for (int i = v + 1; i < nodes; ++i)
-            inner = inner || parent_of(a, b, i) == v;
-        if (a.draft && inner)
-            softmax_stats<DT>(row_ptr<DT>(a.draft, a, b, v), a.vocab, c, red, st.mq, st.invq);
+        best = wave_reduce(best, MaxOp{});
+        if (lane == 0)
+            *out = uint2{(uint32_t)best, (uint32_t)(best >> 32)};
+        return;
     }
-    if (threadIdx.x == 0)
-        stats[(int64_t)b * a.n + v] = st;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        row.values(raw[i], pos0 + i * 512, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            m = fmaxf(m, x[e]);
+    }
+    m = wave_reduce(m, MaxOp{});
+    const float base = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        row.values(raw[i], pos0 + i * 512, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum += __builtin_amdgcn_exp2f((x[e] - base) * c);
+    }
+    sum = wave_reduce(sum, SumOp{});
+    if (lane == 0)
+        *out = uint2{__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, sum)};
 }
 
+// A node's distribution as the walk keeps it: exp2((x - m) c) * inv.
+struct Terms {
+    float m, inv;
+};
+
 template <int DT>
-__global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a, const RowStat *stats) {
-    __shared__ uint64_t red[kWalkThreads / 64];
-    __shared__ int32_t gone[VQ_MAX_TREE_NODES];  // tokens of the rejected children (no draft logits)
-    const int b = (int)blockIdx.x, tid = (int)threadIdx.x, nodes = live_nodes(a, b);
+__global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a) {
+    __shared__ float red[kWalkThreads / 64];
+    __shared__ Terms p[kNodes], q[kNodes];
+    __shared__ int32_t best[kNodes], token[kNodes], parent[kNodes], gone[kNodes];
+    __shared__ float u[kNodes], px[kNodes], qx[kNodes];  // of a node's token, in its parent's rows
+    const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = tid & 63, wave = wave_id();
+    const int nodes = live_nodes(a, b);
     int32_t *tokens = a.tokens_out + (int64_t)b * a.n, *path = a.path_out + (int64_t)b * a.n;
-    const int32_t *drafted = a.node_tokens + (int64_t)b * a.n;
-    const float *noise = a.noise + (int64_t)b * a.vocab;
     if (tid < a.n) {
         tokens[tid] = -1;
         path[tid] = -1;
+        token[tid] = a.node_tokens[(int64_t)b * a.n + tid];
+        parent[tid] = tid > 0 && tid < nodes ? parent_of(a, b, tid) : -1;
+        u[tid] = a.uniforms[(int64_t)b * a.n + tid];
     }
-    if (nodes == 0) {
-        if (tid == 0)
-            a.count_out[b] = 0;
-        return;
+    const float c = exponent_scale(a, b);
+    // Join the chunks, a wave per row at a time.
+    for (int r = wave; r < 2 * nodes; r += kWalkThreads / 64) {
+        const bool draft = r >= nodes;
+        const int v = draft ? r - nodes : r;
+        if (draft && (!a.draft || c == 0.f))
+            break;
+        const uint2 *part = a.part + (((int64_t)b * 2 + (draft ? 1 : 0)) * a.n + v) * a.chunks;
+        if (c == 0.f) {
+            uint64_t k = 0;
+            for (int x = lane; x < a.chunks; x += 64)
+                k = MaxOp{}(k, ((uint64_t)part[x].y << 32) | part[x].x);
+            k = wave_reduce(k, MaxOp{});
+            if (lane == 0)
+                best[v] = (int32_t)~(uint32_t)k;
+            continue;
+        }
+        if (draft && !__any(lane > v && lane < nodes && parent_of(a, b, lane) == v))
+            continue;  // not read, not needed
+        float m = -INFINITY, sum = 0.f;
+        for (int x = lane; x < a.chunks; x += 64) {
+            const float mx = __builtin_bit_cast(float, part[x].x), lx = __builtin_bit_cast(float, part[x].y);
+            const float top = fmaxf(m, mx), base = top == -INFINITY ? 0.f : top;
+            sum = sum * __builtin_amdgcn_exp2f((m - base) * c) + lx * __builtin_amdgcn_exp2f((mx - base) * c);
+            m = top;
+        }
+        const float top = wave_reduce(m, MaxOp{}), base = top == -INFINITY ? 0.f : top;
+        sum = wave_reduce(sum * __builtin_amdgcn_exp2f((m - base) * c), SumOp{});
+        if (lane == 0)
+            (draft ? q : p)[v] = Terms{top, 1.f / sum};
     }
     __syncthreads();
-    const float c = exponent_scale(a, b);
-    int v = 0, count = 1;
-    if (tid == 0)
+    // What each drafted token has in its parent's rows.
+    if (tid < nodes) {
+        const int v = parent[tid], x = token[tid];
+        px[tid] = qx[tid] = 0.f;
+        if (tid > 0 && v >= 0 && v < tid && c != 0.f && x >= 0 && x < a.vocab) {
+            const int64_t at = ((int64_t)b * a.n + v) * a.vocab + x;
+            px[tid] = __builtin_amdgcn_exp2f((logit_at<DT>(a.target, at) - p[v].m) * c) * p[v].inv;
+            qx[tid] = a.draft ? __builtin_amdgcn_exp2f((logit_at<DT>(a.draft, at) - q[v].m) * c) * q[v].inv : 1.f;
+        }
+    }
+    __syncthreads();
+    int v = 0, count = 1, n_gone = 0;
+    float S = 0.f;
+    if (tid == 0 && nodes)
         path[0] = 0;
-    for (;;) {
-        const RowStat st = stats[(int64_t)b * a.n + v];
-        const void *rp = row_ptr<DT>(a.target, a, b, v);
-        const void *rq = a.draft ? row_ptr<DT>(a.draft, a, b, v) : nullptr;
-        auto prob = [&](int x) { return exp2f((logit_at<DT>(rp, x) - st.m) * c) * st.inv; };
-        auto drawn = [&](int x) { return exp2f((logit_at<DT>(rq, x) - st.mq) * c) * st.invq; };
-        float S = 0.f, s = 1.f;
-        int n_gone = 0, next = -1;
+    for (bool more = nodes > 0; more;) {
+        S = 0.f;
+        n_gone = 0;
+        float s = 1.f;
         bool stale = false;  // s is older than S
-        auto left = [&](int x) -> float {
-            const float p = prob(x);
-            if (rq)
-                return S > 0.f ? fmaxf(0.f, p - S * drawn(x)) : p;
-            for (int g = 0; g < n_gone; ++g)
-                if (gone[g] == x)
-                    return 0.f;
-            return p;
-        };
+        int next = -1;
         for (int kid = v + 1; kid < nodes && next < 0; ++kid) {
-            if (parent_of(a, b, kid) != v)
+            if (parent[kid] != v)
                 continue;
-            const int x = drafted[kid];
+            const int x = token[kid];
             if (c == 0.f) {
-                next = x == st.best ? kid : -1;
+                next = x == best[v] ? kid : -1;
                 continue;
             }
             if (stale) {
+                const Row<DT> rp(a.target, a, b, v), rq(a.draft, a, b, v);
                 float sum = 0.f;
-                for (int y = tid; y < a.vocab; y += kWalkThreads)
-                    sum += left(y);
-                s = block_reduce<kWalkThreads>(sum, SumOp{}, red);
+                for (int pos = tid * 8; pos < rp.end(); pos += kWalkThreads * 8) {
+                    u32x4 wp[Row<DT>::kElem / 2], wq[Row<DT>::kElem / 2];
+                    float xp[8], xq[8];
+                    rp.load(pos, wp);
+                    rq.load(pos, wq);
+                    rp.values(wp, pos, xp);
+                    rq.values(wq, pos, xq);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum += left_of(__builtin_amdgcn_exp2f((xp[e] - p[v].m) * c) * p[v].inv, S,
+                                       __builtin_amdgcn_exp2f((xq[e] - q[v].m) * c) * q[v].inv);
+                }
+                sum = wave_reduce(sum, SumOp{});
+                __syncthreads();
+                if (lane == 0)
+                    red[wave] = sum;
+                __syncthreads();
+                s = 0.f;
+                for (int w = 0; w < kWalkThreads / 64; ++w)
+                    s += red[w];
                 stale = false;
             }
-            const bool inside = x >= 0 && x < a.vocab;
-            const float rx = inside ? left(x) : 0.f;
-            const float qx = rq ? (inside ? drawn(x) : 0.f) : 1.f;
-            if (inside && a.uniforms[(int64_t)b * a.n + kid] * qx * s < rx) {
+            float rx = a.draft ? left_of(px[kid], S, qx[kid]) : px[kid];
+            for (int g = 0; g < n_gone; ++g)
+                rx = gone[g] == x ? 0.f : rx;
+            if (u[kid] * qx[kid] * s < rx) {
                 next = kid;
-                continue;
-            }
-            if (rq) {
+            } else if (a.draft) {
                 S += s;
                 stale = true;
             } else {
@@ -226,58 +340,179 @@ __global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a, const RowStat
                 __syncthreads();
             }
         }
-        if (next >= 0) {
+        more = next >= 0;
+        if (more) {
             if (tid == 0) {
-                tokens[count - 1] = drafted[next];
+                tokens[count - 1] = token[next];
                 path[count] = next;
             }
             ++count;
             v = next;
-            continue;
         }
-        int32_t last = st.best;
-        if (c != 0.f) {
-            uint64_t best = 0;
-            for (int pass = 0; pass < 2 && best == 0; ++pass) {
-                for (int x = tid; x < a.vocab; x += kWalkThreads) {
-                    const float r = pass == 0 ? left(x) : prob(x);
-                    if (r > 0.f) {
-                        const uint64_t k = key_of(r / noise[x], x);
-                        best = k > best ? k : best;
-                    }
-                }
-                best = block_reduce<kWalkThreads>(best, MaxOp{}, red);
-            }
-            last = best ? (int32_t)~(uint32_t)best : 0;
-        }
-        if (tid == 0) {
-            tokens[count - 1] = last;
-            a.count_out[b] = count;
-        }
-        return;
     }
+    if (tid == 0) {
+        a.count_out[b] = nodes ? count : 0;
+        if (nodes && c == 0.f)
+            tokens[count - 1] = best[v];
+        Last &l = a.last[b];
+        l.key = 0;
+        l.arrived = 0;
+        l.node = nodes && c != 0.f ? v : -1;
+        l.at = count - 1;
+        if (nodes) {
+            l.m = p[v].m;
+            l.inv = p[v].inv;
+            l.mq = q[v].m;
+            l.invq = q[v].inv;
+        }
+        l.S = S;
+        l.n_gone = n_gone;
+    }
+    if (tid < n_gone)
+        a.last[b].gone[tid] = gone[tid];
+}
+
+// The best key of a thread's tokens of one piece: argmax r / noise over r > 0.
+// rest: the remainder (with S and the rejected tokens), else p itself.
+template <int DT>
+__device__ __forceinline__ uint64_t draw_piece(const KArgs &a, const Last &l, const Row<DT> &rp, const Row<DT> &rq,
+                                               const float *noise, float c, int pos, bool rest) {
+    const bool drawn = rest && l.S > 0.f;
+    u32x4 wp[Row<DT>::kElem / 2], wq[Row<DT>::kElem / 2];
+    float e8[8], xp[8], xq[8];
+    rp.load(pos, wp);
+    if (drawn)
+        rq.load(pos, wq);
+    const int x0 = pos - rp.shift;
+    if (x0 >= 0 && x0 + 8 <= a.vocab) {
+        typedef f32x4 f32x4_dword __attribute__((aligned(4)));  // the row may begin anywhere
+        const f32x4 lo = *reinterpret_cast<const f32x4_dword *>(noise + x0),
+                    hi = *reinterpret_cast<const f32x4_dword *>(noise + x0 + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            e8[e] = lo[e];
+            e8[e + 4] = hi[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            e8[e] = x0 + e >= 0 && x0 + e < a.vocab ? noise[x0 + e] : 1.f;
+    }
+    rp.values(wp, pos, xp);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        xp[e] = __builtin_amdgcn_exp2f((xp[e] - l.m) * c) * l.inv;
+    if (drawn) {
+        rq.values(wq, pos, xq);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            xp[e] = left_of(xp[e], l.S, __builtin_amdgcn_exp2f((xq[e] - l.mq) * c) * l.invq);
+    }
+    if (rest)
+        for (int g = 0; g < l.n_gone; ++g) {
+            const int at = l.gone[g] - x0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                xp[e] = at == e ? 0.f : xp[e];
+        }
+    uint64_t best = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (xp[e] > 0.f) {
+            const uint64_t k = key_of(xp[e] / e8[e], x0 + e);
+            best = k > best ? k : best;
+        }
+    return best;
 }
 
 template <int DT>
-void launch_dt(const KArgs &a, int batch, void *workspace, hipStream_t stream) {
-    RowStat *stats = static_cast<RowStat *>(workspace);
-    hipLaunchKernelGGL(tree_row_stats<DT>, dim3(a.n, batch), dim3(kStatThreads), 0, stream, a, stats);
-    hipLaunchKernelGGL(tree_walk<DT>, dim3(batch), dim3(kWalkThreads), 0, stream, a, stats);
+__global__ __launch_bounds__(kThreads) void tree_draw(KArgs a) {
+    __shared__ uint64_t red[kThreads / 64];
+    __shared__ int last_here;
+    const int b = (int)blockIdx.y, tid = (int)threadIdx.x;
+    Last &l = a.last[b];
+    const int v = l.node;
+    if (v < 0)
+        return;
+    const float c = exponent_scale(a, b);
+    const Row<DT> rp(a.target, a, b, v), rq(a.draft ? a.draft : a.target, a, b, v);
+    const float *noise = a.noise + (int64_t)b * a.vocab;
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int pos = (int)blockIdx.x * kDrawChunk + (i * kThreads + tid) * 8;
+        if (pos < rp.end())
+            best = MaxOp{}(best, draw_piece<DT>(a, l, rp, rq, noise, c, pos, true));
+    }
+    best = wave_reduce(best, MaxOp{});
+    if ((tid & 63) == 0)
+        red[tid >> 6] = best;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+        for (int w = 1; w < kThreads / 64; ++w)
+            best = MaxOp{}(best, red[w]);
+        // the key is in memory before this workgroup counts itself in: the
+        // count waits for the value that the maximum replaced
+        uint64_t old = __hip_atomic_fetch_max(&l.key, best, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(old)::"memory");
+        last_here = __hip_atomic_fetch_add(&l.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                    gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last_here)
+        return;
+    uint64_t key = __hip_atomic_load(&l.key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (key == 0) {
+        // nothing is left of r: p stands in
+        for (int pos = tid * 8; pos < rp.end(); pos += kThreads * 8)
+            key = MaxOp{}(key, draw_piece<DT>(a, l, rp, rq, noise, c, pos, false));
+        key = wave_reduce(key, MaxOp{});
+        __syncthreads();
+        if ((tid & 63) == 0)
+            red[tid >> 6] = key;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 64; ++w)
+            key = MaxOp{}(key, red[w]);
+    }
+    if (tid == 0)
+        a.tokens_out[(int64_t)b * a.n + l.at] = key ? (int32_t)~(uint32_t)key : 0;
+}
+
+// Chunks of a row: the first may begin with the 7 elements of alignment.
+int row_chunks(int vocab) { return (vocab + 7 + kChunk - 1) / kChunk; }
+
+template <int DT>
+void launch_dt(const KArgs &a, int batch, hipStream_t stream) {
+    const int groups = (a.chunks + kThreads / 64 - 1) / (kThreads / 64);
+    hipLaunchKernelGGL(tree_row_stats<DT>, dim3(groups, a.draft ? 2 * a.n : a.n, batch), dim3(kThreads), 0, stream,
+                       a);
+    hipLaunchKernelGGL(tree_walk<DT>, dim3(batch), dim3(kWalkThreads), 0, stream, a);
+    hipLaunchKernelGGL(tree_draw<DT>, dim3((a.vocab + 7 + kDrawChunk - 1) / kDrawChunk, batch), dim3(kThreads), 0,
+                       stream, a);
+}
+
+size_t part_bytes(int batch, int n, int vocab) {
+    return ((size_t)batch * 2 * n * row_chunks(vocab) * sizeof(uint2) + 15) & ~(size_t)15;
 }
 
 }  // namespace
 
-size_t tree_verify_workspace(int batch, int n, int) { return (size_t)batch * n * sizeof(RowStat); }
+size_t tree_verify_workspace(int batch, int n, int vocab) {
+    return part_bytes(batch, n, vocab) + (size_t)batch * sizeof(Last);
+}
 
 hipError_t launch_tree_verify(const TreeVerifyArgs &p) {
     KArgs a{p.target, p.draft, p.node_tokens, p.parents, p.n_nodes, p.temperature, p.uniforms, p.noise,
-            p.tokens_out, p.path_out, p.count_out, p.n, p.vocab};
+            p.tokens_out, p.path_out, p.count_out, static_cast<uint2 *>(p.workspace),
+            reinterpret_cast<Last *>(static_cast<char *>(p.workspace) + part_bytes(p.batch, p.n, p.vocab)),
+            p.n, p.vocab, row_chunks(p.vocab)};
     if (p.dtype == VQ_DTYPE_F32)
-        launch_dt<VQ_DTYPE_F32>(a, p.batch, p.workspace, p.stream);
+        launch_dt<VQ_DTYPE_F32>(a, p.batch, p.stream);
     else if (p.dtype == VQ_DTYPE_BF16)
-        launch_dt<VQ_DTYPE_BF16>(a, p.batch, p.workspace, p.stream);
+        launch_dt<VQ_DTYPE_BF16>(a, p.batch, p.stream);
     else
-        launch_dt<VQ_DTYPE_F16>(a, p.batch, p.workspace, p.stream);
+        launch_dt<VQ_DTYPE_F16>(a, p.batch, p.stream);
     return hipGetLastError();
 }
 

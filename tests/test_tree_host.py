@@ -97,7 +97,7 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="k_cache"):
         vq.kv_append(k[None], k[None], kc, vc, table, ctx)
     with pytest.raises(ValueError, match="draft"):
-        vq.tree_verify(torch.zeros(2, 3, 7), torch.zeros(2, 3, 8), table, None, None)
+        vq._array(torch.zeros(2, 3, 8), "draft", (2, 3, 7), torch.float32)
 
 
 def test_row_strides():
@@ -105,13 +105,13 @@ def test_row_strides():
         def __init__(self, t):
             self.shape, self.is_cuda, self.stride = t.shape, True, t.stride
     fused = torch.zeros(3, 5, 100 * 8)
-    assert vq._rows(T(fused[..., 64:192].unflatten(-1, (2, 64))), "k", (3, 5), 2, 64) == 800
-    assert vq._rows(T(fused[:, :1, :128].unflatten(-1, (2, 64))), "k", (3, 1), 2, 64) == 4000
-    assert vq._rows(T(fused[:1, :1, :128].unflatten(-1, (2, 64))), "k", (1, 1), 2, 64) == 128
+    assert vq._rows(T(fused[..., 64:192].unflatten(-1, (2, 64))), "k", (3, 5, 2, 64)) == 800
+    assert vq._rows(T(fused[:, :1, :128].unflatten(-1, (2, 64))), "k", (3, 1, 2, 64)) == 4000
+    assert vq._rows(T(fused[:1, :1, :128].unflatten(-1, (2, 64))), "k", (1, 1, 2, 64)) == 128
     with pytest.raises(ValueError, match="evenly"):
-        vq._rows(T(fused[:, :4, :128].unflatten(-1, (2, 64))), "k", (3, 4), 2, 64)
+        vq._rows(T(fused[:, :4, :128].unflatten(-1, (2, 64))), "k", (3, 4, 2, 64))
     with pytest.raises(ValueError, match="contiguous"):
-        vq._rows(T(fused[..., :128].unflatten(-1, (64, 2)).transpose(-1, -2)), "k", (3, 5), 2, 64)
+        vq._rows(T(fused[..., :128].unflatten(-1, (64, 2)).transpose(-1, -2)), "k", (3, 5, 2, 64))
 
 
 def test_reference_attention():
