@@ -11,7 +11,7 @@
 // with probability r_x / sum r, so no running sum over the vocabulary is
 // compared with a threshold, and the result does not hang on its rounding.
 //
-// Three kernels.  The first reads every row once, a wave per chunk of 2048
+// Three kernels.  The first reads every row once, a workgroup per chunk of 8192
 // logits held in registers, and leaves each chunk's maximum and sum of
 // exponentials (or, for a greedy sequence, its best key).  The second, one
 // workgroup per sequence, joins the chunks, looks the drafted tokens up and
@@ -29,7 +29,8 @@ constexpr int kNodes = VQ_MAX_TREE_NODES;
 constexpr int kThreads = 256;
 constexpr int kWalkThreads = 1024;
 constexpr int kPieces = 4;                   // pieces of 8 logits a lane holds
-constexpr int kChunk = 64 * 8 * kPieces;     // logits of a wave of the first kernel
+constexpr int kChunk = kThreads * 8 * kPieces;  // logits of a workgroup of the first kernel
+constexpr int kJoinLanes = 16;               // lanes that join a row's chunks in the second
 constexpr int kDrawChunk = kThreads * 8 * 2;  // tokens of a workgroup of the third
 
 struct KArgs {
@@ -78,10 +79,11 @@ __device__ __forceinline__ uint64_t lane_xor(uint64_t x, int off) {
     return ((uint64_t)hi << 32) | lo;
 }
 
-template <typename Op, typename T>
+// Reduction over runs of LANES lanes (all of a run active); each gets it.
+template <int LANES, typename Op, typename T>
 __device__ __forceinline__ T wave_reduce(T x, Op op) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
+    for (int off = LANES / 2; off >= 1; off >>= 1)
         x = op(x, lane_xor(x, off));
     return x;
 }
@@ -156,10 +158,11 @@ struct Row {
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void tree_row_stats(KArgs a) {
-    const int lane = (int)(threadIdx.x & 63), chunk = (int)blockIdx.x * (kThreads / 64) + wave_id();
+    __shared__ uint64_t red[kThreads / 64];
+    const int lane = (int)(threadIdx.x & 63), wave = wave_id(), chunk = (int)blockIdx.x;
     const bool draft = (int)blockIdx.y >= a.n;
     const int v = (int)blockIdx.y - (draft ? a.n : 0), b = (int)blockIdx.z, nodes = live_nodes(a, b);
-    if (v >= nodes || chunk >= a.chunks)
+    if (v >= nodes)
         return;
     const float c = exponent_scale(a, b);
     if (draft) {
@@ -169,17 +172,17 @@ __global__ __launch_bounds__(kThreads) void tree_row_stats(KArgs a) {
     }
     const Row<DT> row(draft ? a.draft : a.target, a, b, v);
     u32x4 raw[kPieces][Row<DT>::kElem / 2];
-    const int pos0 = chunk * kChunk + lane * 8;
+    const int pos0 = chunk * kChunk + (int)threadIdx.x * 8;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-        row.load(pos0 + i * 512, raw[i]);
+        row.load(pos0 + i * kThreads * 8, raw[i]);
     uint2 *out = a.part + (((int64_t)b * 2 + (draft ? 1 : 0)) * a.n + v) * a.chunks + chunk;
     float x[8];
     if (c == 0.f) {
         uint64_t best = 0;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int pos = pos0 + i * 512;
+            const int pos = pos0 + i * kThreads * 8;
             row.values(raw[i], pos, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -188,32 +191,53 @@ __global__ __launch_bounds__(kThreads) void tree_row_stats(KArgs a) {
                     best = k > best ? k : best;
             }
         }
-        best = wave_reduce(best, MaxOp{});
+        best = wave_reduce<64>(best, MaxOp{});
         if (lane == 0)
+            red[wave] = best;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w)
+            best = MaxOp{}(best, red[w]);
+        if (threadIdx.x == 0)
             *out = uint2{(uint32_t)best, (uint32_t)(best >> 32)};
         return;
     }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        row.values(raw[i], pos0 + i * 512, x);
+        row.values(raw[i], pos0 + i * kThreads * 8, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             m = fmaxf(m, x[e]);
     }
-    m = wave_reduce(m, MaxOp{});
+    // each wave by its own maximum, then the four
+    m = wave_reduce<64>(m, MaxOp{});
     const float base = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        row.values(raw[i], pos0 + i * 512, x);
+        row.values(raw[i], pos0 + i * kThreads * 8, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             sum += __builtin_amdgcn_exp2f((x[e] - base) * c);
     }
-    sum = wave_reduce(sum, SumOp{});
+    sum = wave_reduce<64>(sum, SumOp{});
+    float2 *mine = reinterpret_cast<float2 *>(red);
     if (lane == 0)
-        *out = uint2{__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, sum)};
+        mine[wave] = float2{m, sum};
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float top = m;
+#pragma unroll
+        for (int w = 1; w < kThreads / 64; ++w)
+            top = fmaxf(top, mine[w].x);
+        const float all = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w)
+            sum += mine[w].y * __builtin_amdgcn_exp2f((mine[w].x - all) * c);
+        *out = uint2{__builtin_bit_cast(uint32_t, top), __builtin_bit_cast(uint32_t, sum)};
+    }
 }
 
 // A node's distribution as the walk keeps it: exp2((x - m) c) * inv.
@@ -230,6 +254,7 @@ __global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a) {
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = tid & 63, wave = wave_id();
     const int nodes = live_nodes(a, b);
     int32_t *tokens = a.tokens_out + (int64_t)b * a.n, *path = a.path_out + (int64_t)b * a.n;
+    const float c = exponent_scale(a, b);
     if (tid < a.n) {
         tokens[tid] = -1;
         path[tid] = -1;
@@ -237,36 +262,32 @@ __global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a) {
         parent[tid] = tid > 0 && tid < nodes ? parent_of(a, b, tid) : -1;
         u[tid] = a.uniforms[(int64_t)b * a.n + tid];
     }
-    const float c = exponent_scale(a, b);
-    // Join the chunks, a wave per row at a time.
-    for (int r = wave; r < 2 * nodes; r += kWalkThreads / 64) {
-        const bool draft = r >= nodes;
-        const int v = draft ? r - nodes : r;
-        if (draft && (!a.draft || c == 0.f))
-            break;
-        const uint2 *part = a.part + (((int64_t)b * 2 + (draft ? 1 : 0)) * a.n + v) * a.chunks;
+    // Join the chunks, sixteen lanes per row; the rows of leaves' drafters
+    // hold nothing and are not looked at later.
+    const int rows = a.draft && c != 0.f ? 2 * nodes : nodes;
+    for (int r = tid / kJoinLanes; r < rows; r += kWalkThreads / kJoinLanes) {
+        const int v = r < nodes ? r : r - nodes, sub = tid % kJoinLanes;
+        const uint2 *part = a.part + (((int64_t)b * 2 + (r < nodes ? 0 : 1)) * a.n + v) * a.chunks;
         if (c == 0.f) {
             uint64_t k = 0;
-            for (int x = lane; x < a.chunks; x += 64)
+            for (int x = sub; x < a.chunks; x += kJoinLanes)
                 k = MaxOp{}(k, ((uint64_t)part[x].y << 32) | part[x].x);
-            k = wave_reduce(k, MaxOp{});
-            if (lane == 0)
+            k = wave_reduce<kJoinLanes>(k, MaxOp{});
+            if (sub == 0)
                 best[v] = (int32_t)~(uint32_t)k;
             continue;
         }
-        if (draft && !__any(lane > v && lane < nodes && parent_of(a, b, lane) == v))
-            continue;  // not read, not needed
         float m = -INFINITY, sum = 0.f;
-        for (int x = lane; x < a.chunks; x += 64) {
+        for (int x = sub; x < a.chunks; x += kJoinLanes) {
             const float mx = __builtin_bit_cast(float, part[x].x), lx = __builtin_bit_cast(float, part[x].y);
             const float top = fmaxf(m, mx), base = top == -INFINITY ? 0.f : top;
             sum = sum * __builtin_amdgcn_exp2f((m - base) * c) + lx * __builtin_amdgcn_exp2f((mx - base) * c);
             m = top;
         }
-        const float top = wave_reduce(m, MaxOp{}), base = top == -INFINITY ? 0.f : top;
-        sum = wave_reduce(sum * __builtin_amdgcn_exp2f((m - base) * c), SumOp{});
-        if (lane == 0)
-            (draft ? q : p)[v] = Terms{top, 1.f / sum};
+        const float top = wave_reduce<kJoinLanes>(m, MaxOp{}), base = top == -INFINITY ? 0.f : top;
+        sum = wave_reduce<kJoinLanes>(sum * __builtin_amdgcn_exp2f((m - base) * c), SumOp{});
+        if (sub == 0)
+            (r < nodes ? p : q)[v] = Terms{top, 1.f / sum};
     }
     __syncthreads();
     // What each drafted token has in its parent's rows.
@@ -301,19 +322,25 @@ __global__ __launch_bounds__(kWalkThreads) void tree_walk(KArgs a) {
             if (stale) {
                 const Row<DT> rp(a.target, a, b, v), rq(a.draft, a, b, v);
                 float sum = 0.f;
-                for (int pos = tid * 8; pos < rp.end(); pos += kWalkThreads * 8) {
-                    u32x4 wp[Row<DT>::kElem / 2], wq[Row<DT>::kElem / 2];
-                    float xp[8], xq[8];
-                    rp.load(pos, wp);
-                    rq.load(pos, wq);
-                    rp.values(wp, pos, xp);
-                    rq.values(wq, pos, xq);
+                for (int pos = tid * 8; pos < rp.end(); pos += kPieces * kWalkThreads * 8) {
+                    u32x4 wp[kPieces][Row<DT>::kElem / 2], wq[kPieces][Row<DT>::kElem / 2];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum += left_of(__builtin_amdgcn_exp2f((xp[e] - p[v].m) * c) * p[v].inv, S,
-                                       __builtin_amdgcn_exp2f((xq[e] - q[v].m) * c) * q[v].inv);
+                    for (int i = 0; i < kPieces; ++i) {  // past the row: zeros, left out as -inf
+                        rp.load(pos + i * kWalkThreads * 8, wp[i]);
+                        rq.load(pos + i * kWalkThreads * 8, wq[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        float xp[8], xq[8];
+                        rp.values(wp[i], pos + i * kWalkThreads * 8, xp);
+                        rq.values(wq[i], pos + i * kWalkThreads * 8, xq);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            sum += left_of(__builtin_amdgcn_exp2f((xp[e] - p[v].m) * c) * p[v].inv, S,
+                                           __builtin_amdgcn_exp2f((xq[e] - q[v].m) * c) * q[v].inv);
+                    }
                 }
-                sum = wave_reduce(sum, SumOp{});
+                sum = wave_reduce<64>(sum, SumOp{});
                 __syncthreads();
                 if (lane == 0)
                     red[wave] = sum;
@@ -444,7 +471,7 @@ __global__ __launch_bounds__(kThreads) void tree_draw(KArgs a) {
         if (pos < rp.end())
             best = MaxOp{}(best, draw_piece<DT>(a, l, rp, rq, noise, c, pos, true));
     }
-    best = wave_reduce(best, MaxOp{});
+    best = wave_reduce<64>(best, MaxOp{});
     if ((tid & 63) == 0)
         red[tid >> 6] = best;
     __syncthreads();
@@ -467,7 +494,7 @@ __global__ __launch_bounds__(kThreads) void tree_draw(KArgs a) {
         // nothing is left of r: p stands in
         for (int pos = tid * 8; pos < rp.end(); pos += kThreads * 8)
             key = MaxOp{}(key, draw_piece<DT>(a, l, rp, rq, noise, c, pos, false));
-        key = wave_reduce(key, MaxOp{});
+        key = wave_reduce<64>(key, MaxOp{});
         __syncthreads();
         if ((tid & 63) == 0)
             red[tid >> 6] = key;
@@ -484,8 +511,7 @@ int row_chunks(int vocab) { return (vocab + 7 + kChunk - 1) / kChunk; }
 
 template <int DT>
 void launch_dt(const KArgs &a, int batch, hipStream_t stream) {
-    const int groups = (a.chunks + kThreads / 64 - 1) / (kThreads / 64);
-    hipLaunchKernelGGL(tree_row_stats<DT>, dim3(groups, a.draft ? 2 * a.n : a.n, batch), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(tree_row_stats<DT>, dim3(a.chunks, a.draft ? 2 * a.n : a.n, batch), dim3(kThreads), 0, stream,
                        a);
     hipLaunchKernelGGL(tree_walk<DT>, dim3(batch), dim3(kWalkThreads), 0, stream, a);
     hipLaunchKernelGGL(tree_draw<DT>, dim3((a.vocab + 7 + kDrawChunk - 1) / kDrawChunk, batch), dim3(kThreads), 0,
