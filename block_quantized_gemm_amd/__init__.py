@@ -140,13 +140,19 @@ def _torch():
     return torch
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32,
-         torch.int8: DTYPE_I8}
-    if t.dtype not in m:
-        raise TypeError("unsupported dtype %s" % t.dtype)
-    return m[t.dtype]
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        torch = _torch()
+        _dtype_codes.update({torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32,
+                             torch.int8: DTYPE_I8})
+        code = _dtype_codes.get(t.dtype)
+        if code is None:
+            raise TypeError("unsupported dtype %s" % t.dtype)
+    return code
 
 
 def _dev_ptr(t, name: str) -> int:
@@ -720,8 +726,10 @@ def _rows(t, name: str, shape) -> int:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    st = t.stride()
     heads, dim = shape[-2:]
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
     if st[-1] != 1 or (heads > 1 and st[-2] != dim):
         raise ValueError("%s: the heads and channels of a row must be contiguous" % name)
     row, rows = 0, 1
@@ -739,11 +747,9 @@ def _array(t, name: str, shape, dtype):
     """Device pointer of a contiguous array, or NULL for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError("%s must be %s %s" % (name, dtype, tuple(shape)))
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("%s must be a contiguous device tensor" % name)
-    return t.data_ptr()
+    if t.shape == shape and t.dtype == dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous device tensor, %s %s" % (name, dtype, tuple(shape)))
 
 
 def _cache(k_cache, v_cache, lead, dtype):
