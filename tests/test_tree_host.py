@@ -103,7 +103,7 @@ def test_binding_refusals():
 def test_row_strides():
     class T:  # a tensor of this shape and strides on a device
         def __init__(self, t):
-            self.shape, self.is_cuda, self.stride = t.shape, True, t.stride
+            self.shape, self.is_cuda, self.stride, self.is_contiguous = t.shape, True, t.stride, t.is_contiguous
     fused = torch.zeros(3, 5, 100 * 8)
     assert vq._rows(T(fused[..., 64:192].unflatten(-1, (2, 64))), "k", (3, 5, 2, 64)) == 800
     assert vq._rows(T(fused[:, :1, :128].unflatten(-1, (2, 64))), "k", (3, 1, 2, 64)) == 4000
