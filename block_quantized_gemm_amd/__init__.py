@@ -698,6 +698,18 @@ def _raw_stream(stream) -> int:
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _empty(shape, dtype, device, stream):
+    """An output allocated by a call: it belongs to the stream the call runs
+    on, so that memory torch reuses for it is free there."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _stream_workspace(name: str, workspace, need: int, device, stream_handle: int):
     """The Workspace of a call that always needs one: the caller's, or ("auto")
     one cached per operator, device and stream, grown to `need` bytes."""
@@ -795,7 +807,7 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, ctx_len, *, tree_mask=
         raise ValueError("page_table must be [batch][max_pages]")
     W = page_table.shape[1]
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype, q.device, stream)
     L, sh, i32 = lib(), _raw_stream(stream), torch.int32
     ws = _stream_workspace("tree_attention", workspace,
                            L.vq_tree_attention_workspace_bytes(B, n, Hq, H, D), q.device, sh)
@@ -838,11 +850,11 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
     shape = B, n, V = tuple(target.shape)
     i32, f32, dev = torch.int32, torch.float32, target.device
     if tokens_out is None:
-        tokens_out = torch.empty((B, n), dtype=i32, device=dev)
+        tokens_out = _empty((B, n), i32, dev, stream)
     if path_out is None:
-        path_out = torch.empty((B, n), dtype=i32, device=dev)
+        path_out = _empty((B, n), i32, dev, stream)
     if count_out is None:
-        count_out = torch.empty((B,), dtype=i32, device=dev)
+        count_out = _empty((B,), i32, dev, stream)
     L, sh = lib(), _raw_stream(stream)
     ws = _stream_workspace("tree_verify", workspace, L.vq_tree_verify_workspace_bytes(B, n, V), dev, sh)
     st = L.vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
@@ -879,7 +891,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
         raise ValueError("page_table must be [batch][max_pages]")
     W, i32 = page_table.shape[1], torch.int32
     if len_out is None:
-        len_out = torch.empty((B,), dtype=i32, device=k.device)
+        len_out = _empty((B,), i32, k.device, stream)
     st = lib().vq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _dev_ptr(k_cache, "k_cache"),
                             _dev_ptr(v_cache, "v_cache"), _array(page_table, "page_table", (B, W), i32),
                             _array(ctx_len, "ctx_len", (B,), i32), _array(path, "path", (B, n), i32),

@@ -140,7 +140,7 @@ int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_strid
         return VQ_ERR_BAD_DTYPE;
     if (!heads_ok(batch, kv_heads, head_dim) || !cache_ok(page_size, n_pages, max_pages) ||
         !in(n_layers, 1, VQ_MAX_HEADS) || !in(n, 1, VQ_MAX_DIM) || !stride_ok(k_stride, kv_heads * head_dim) ||
-        !stride_ok(v_stride, kv_heads * head_dim))
+        !stride_ok(v_stride, kv_heads * head_dim) || !vq::kv_append_fits(n_layers, batch, n, kv_heads, head_dim))
         return VQ_ERR_BAD_SHAPE;
     if (!all_aligned({k, v, k_cache, v_cache, page_table, ctx_len, path, count, len_out}))
         return VQ_ERR_MISALIGNED;

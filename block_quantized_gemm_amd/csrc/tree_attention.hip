@@ -25,6 +25,23 @@
 // workgroup take its steps in turn and join through LDS; a pair cut by a range
 // boundary leaves its pieces (m, l, O in fp32) in the workspace, and a second
 // kernel joins them in order.
+//
+// Measured on one MI355X (whole call, bf16 unless noted; bytes = the cached
+// keys and values once):
+//   1 sequence, 8-node chain, 509 tokens, 64 / 8 heads of 128     22.9 us
+//   32 sequences, single tokens, up to 4k, 32 / 8 of 64, f16      47.1 us  2.9 TB/s
+//   8 sequences, 16-node trees, up to 16k, 64 / 8 of 128         142.5 us  2.3 TB/s
+//   1 sequence, 16-node tree, 128k, 64 / 8 of 128                210.7 us  2.6 TB/s
+//   4 sequences, 61-node trees, up to 8k, 32 / 4 of 256, f16     254.9 us
+// What bounds them: with more rows than a workgroup holds (32, or 16 at D =
+// 256) every group of rows reads the keys and values again, so the 128-row
+// calls move four times the bytes, 10 TB/s out of L2 and the Infinity Cache;
+// the 61-node call reads them 31 times.  Few rows: the page number of a step is
+// read by a vector load and waited for, which also waits for the step's
+// operands already on their way, so a wave has one step in flight; then the
+// start (3 to 4 us: the scan, the first page and operands) and the joining
+// kernel (5 us small, 10 us large).  The short call is the two kernels' 9 us
+// and the host's time to make the call.
 #include <atomic>
 
 #include "tree_internal.h"
@@ -631,8 +648,11 @@ __global__ __launch_bounds__(kThreads) void tree_join_kernel(KArgs a) {
 
 constexpr int kMaxWorkgroups = 1024;
 
-// Tiles of 16 query rows per wave: as many as the rows need, up to what the
-// registers hold beside a step of keys and values.
+// Tiles of 16 query rows per wave: as many as the rows need, up to what 256
+// registers hold beside a step of keys and values (two tiles of D = 128: 64 for
+// O, 64 for the operands, 32 for the scores and probabilities; D = 256 needs 64
+// and 128 for one).  Four tiles would halve the re-reading of 128-row calls and
+// do not fit.
 int row_tiles(int rows, int D) {
     const int most = D == 256 ? 1 : 2;
     return rows <= 16 ? 1 : most;

@@ -59,5 +59,7 @@ struct KvAppendArgs {
     hipStream_t stream;
 };
 hipError_t launch_kv_append(const KvAppendArgs &a);
+// Whether one launch can cover this many rows (the grid holds 2^31 - 1 workgroups).
+bool kv_append_fits(int64_t n_layers, int64_t batch, int64_t n, int64_t kv_heads, int64_t head_dim);
 
 }  // namespace vq

@@ -578,7 +578,7 @@ size_t vq_tree_attention_workspace_bytes(int64_t batch, int64_t n, int64_t q_hea
  *   parents   int32 [batch][n] or NULL (chain); a node i >= 1 whose parent is
  *             not in [0, i) is no node's child
  *   n_nodes   int32 [batch] or NULL (n), taken into [0, n]; 0 gives count 0
- *   temperature fp32 [batch] or NULL (1), >= 0
+ *   temperature fp32 [batch] or NULL (1): 0 or a positive normal number
  *   uniforms  fp32 [batch][n] in [0, 1)
  *   noise     fp32 [batch][vocab], > 0
  *   count_out int32 [batch]: a + 1 for a accepted nodes
@@ -612,7 +612,8 @@ size_t vq_tree_verify_workspace_bytes(int64_t batch, int64_t n, int64_t vocab);
  *   len_out   int32 [batch] or NULL: ctx_len[b] + count[b], at most max_pages *
  *             page_size
  * Every destination is written by one row only as long as no page belongs to
- * two sequences.  Sizes: 1 <= n_layers <= VQ_MAX_HEADS, 1 <= n <= VQ_MAX_DIM.
+ * two sequences.  Sizes: 1 <= n_layers <= VQ_MAX_HEADS, 1 <= n <= VQ_MAX_DIM,
+ * and all rows together within one launch (about 2^45 elements of keys).
  */
 int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype,
                  void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *ctx_len,

@@ -70,7 +70,8 @@ def test_append_refusals():
         assert _append(**{name: 0x10002}) == vq.VQ_ERR_MISALIGNED, name
     assert _append(dt=vq.DTYPE_F32) == vq.VQ_ERR_BAD_DTYPE
     for bad in (dict(layers=0), dict(layers=1025), dict(b=0), dict(n=0), dict(n=(1 << 24) + 1), dict(h=0), dict(d=80),
-                dict(page=33), dict(pages=0), dict(w=0), dict(ks=255), dict(vs=128)):
+                dict(page=33), dict(pages=0), dict(w=0), dict(ks=255), dict(vs=128),
+                dict(layers=1024, b=4096, n=1 << 20, h=2)):
         assert _append(**bad) == vq.VQ_ERR_BAD_SHAPE, bad
 
 
