@@ -698,23 +698,30 @@ def _raw_stream(stream) -> int:
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
-def _empty(shape, dtype, device, stream):
-    """An output allocated by a call: it belongs to the stream the call runs
-    on, so that memory torch reuses for it is free there."""
+def _like(t, stream):
+    """A contiguous output of t's shape, type and device.  It belongs to the
+    stream the call runs on, so that memory torch reuses for it is free there."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _stream_workspace(name: str, workspace, need: int, device, stream_handle: int):
-    """The Workspace of a call that always needs one: the caller's, or ("auto")
-    one cached per operator, device and stream, grown to `need` bytes."""
+_ws_needs = {}
+
+
+def _sized_workspace(query: str, sizes, workspace, device, stream_handle: int):
+    """(pointer, bytes) of the workspace of a call that always needs one of
+    `query`(*sizes) bytes: the caller's Workspace, or ("auto") one cached per
+    operator, device and stream and grown to that."""
     if workspace == "auto":
-        key = (name, device, stream_handle)
+        need = _ws_needs.get((query, sizes))
+        if need is None:
+            need = _ws_needs[(query, sizes)] = int(getattr(lib(), query)(*sizes))
+        key = (query, device, stream_handle)
         ws = _auto_ws.get(key)
         if ws is None or ws.nbytes < need:
             with _auto_lock:
@@ -727,7 +734,7 @@ def _stream_workspace(name: str, workspace, need: int, device, stream_handle: in
     else:
         raise TypeError("workspace must be a Workspace or 'auto'")
     ws.used_on(stream_handle)
-    return ws
+    return ws.ptr(), ws.nbytes
 
 
 def _rows(t, name: str, shape) -> int:
@@ -807,16 +814,15 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, ctx_len, *, tree_mask=
         raise ValueError("page_table must be [batch][max_pages]")
     W = page_table.shape[1]
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
-    L, sh, i32 = lib(), _raw_stream(stream), torch.int32
-    ws = _stream_workspace("tree_attention", workspace,
-                           L.vq_tree_attention_workspace_bytes(B, n, Hq, H, D), q.device, sh)
-    st = L.vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
+        out = _like(q, stream)
+    sh, i32 = _raw_stream(stream), torch.int32
+    wp, wn = _sized_workspace("vq_tree_attention_workspace_bytes", (B, n, Hq, H, D), workspace, q.device, sh)
+    st = lib().vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
                              _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
                              _array(page_table, "page_table", (B, W), i32), _array(ctx_len, "ctx_len", (B,), i32),
                              _array(tree_mask, "tree_mask", (B, n), torch.int64),
                              _array(n_nodes, "n_nodes", (B,), i32), _array(out, "out", shape, dtype), B, n, Hq, H,
-                             D, page, P, W, D ** -0.5 if scale is None else scale, ws.ptr(), ws.nbytes, sh)
+                             D, page, P, W, D ** -0.5 if scale is None else scale, wp, wn, sh)
     _check(st, "vq_tree_attention")
     return out
 
@@ -848,22 +854,24 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
     if target.dim() != 3:
         raise ValueError("target must be [batch][n][vocab]")
     shape = B, n, V = tuple(target.shape)
-    i32, f32, dev = torch.int32, torch.float32, target.device
+    i32, f32 = torch.int32, torch.float32
+    if node_tokens.dim() != 2:
+        raise ValueError("node_tokens must be [batch][n]")
     if tokens_out is None:
-        tokens_out = _empty((B, n), i32, dev, stream)
+        tokens_out = _like(node_tokens, stream)
     if path_out is None:
-        path_out = _empty((B, n), i32, dev, stream)
+        path_out = _like(node_tokens, stream)
     if count_out is None:
-        count_out = _empty((B,), i32, dev, stream)
-    L, sh = lib(), _raw_stream(stream)
-    ws = _stream_workspace("tree_verify", workspace, L.vq_tree_verify_workspace_bytes(B, n, V), dev, sh)
-    st = L.vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
-                          _dtype_code(target), _array(node_tokens, "node_tokens", (B, n), i32),
-                          _array(parents, "parents", (B, n), i32), _array(n_nodes, "n_nodes", (B,), i32),
-                          _array(temperature, "temperature", (B,), f32),
-                          _array(uniforms, "uniforms", (B, n), f32), _array(noise, "noise", (B, V), f32),
-                          _array(tokens_out, "tokens_out", (B, n), i32), _array(path_out, "path_out", (B, n), i32),
-                          _array(count_out, "count_out", (B,), i32), B, n, V, ws.ptr(), ws.nbytes, sh)
+        count_out = _like(node_tokens[:, 0], stream)
+    sh = _raw_stream(stream)
+    wp, wn = _sized_workspace("vq_tree_verify_workspace_bytes", (B, n, V), workspace, target.device, sh)
+    st = lib().vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
+                              _dtype_code(target), _array(node_tokens, "node_tokens", (B, n), i32),
+                              _array(parents, "parents", (B, n), i32), _array(n_nodes, "n_nodes", (B,), i32),
+                              _array(temperature, "temperature", (B,), f32),
+                              _array(uniforms, "uniforms", (B, n), f32), _array(noise, "noise", (B, V), f32),
+                              _array(tokens_out, "tokens_out", (B, n), i32), _array(path_out, "path_out", (B, n), i32),
+                              _array(count_out, "count_out", (B,), i32), B, n, V, wp, wn, sh)
     _check(st, "vq_tree_verify")
     return tokens_out, path_out, count_out
 
@@ -891,7 +899,7 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
         raise ValueError("page_table must be [batch][max_pages]")
     W, i32 = page_table.shape[1], torch.int32
     if len_out is None:
-        len_out = _empty((B,), i32, k.device, stream)
+        len_out = _like(ctx_len, stream)
     st = lib().vq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _dev_ptr(k_cache, "k_cache"),
                             _dev_ptr(v_cache, "v_cache"), _array(page_table, "page_table", (B, W), i32),
                             _array(ctx_len, "ctx_len", (B,), i32), _array(path, "path", (B, n), i32),
