@@ -751,15 +751,17 @@ def _rows(t, name: str, shape) -> int:
     st = t.stride()
     if st[-1] != 1 or (heads > 1 and st[-2] != dim):
         raise ValueError("%s: the heads and channels of a row must be contiguous" % name)
-    row, rows = 0, 1
+    row, rows = None, 1
     for at in range(len(shape) - 3, -1, -1):
         if shape[at] > 1:
-            if row == 0:
+            if row is None:
                 row = st[at]  # every dimension inside this one has size 1
+                if row < heads * dim:  # expanded (stride 0) or overlapping rows
+                    raise ValueError("%s: rows must not share memory" % name)
             elif st[at] != row * rows:
                 raise ValueError("%s: rows must be evenly spaced" % name)
             rows *= shape[at]
-    return row if rows > 1 else heads * dim
+    return heads * dim if row is None else row
 
 
 def _array(t, name: str, shape, dtype):

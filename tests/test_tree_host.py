@@ -115,6 +115,32 @@ def test_row_strides():
         vq._rows(T(fused[..., :128].unflatten(-1, (64, 2)).transpose(-1, -2)), "k", (3, 5, 2, 64))
 
 
+@pytest.mark.parametrize("base,shape", [
+    ((3, 1, 2, 64), (3, 5, 2, 64)), ((1, 1, 2, 64), (3, 5, 2, 64)), ((1, 5, 2, 64), (3, 5, 2, 64)),
+    ((1, 1, 2, 64), (1, 5, 2, 64)), ((1, 1, 2, 64), (3, 1, 2, 64)), ((3, 5, 1, 64), (3, 5, 2, 64)),
+    ((3, 5, 2, 1), (3, 5, 2, 64)), ((4, 3, 1, 2, 64), (4, 3, 5, 2, 64)), ((4, 1, 5, 2, 64), (4, 3, 5, 2, 64)),
+    ((1, 3, 5, 2, 64), (4, 3, 5, 2, 64))])
+def test_expanded_rows_are_refused(base, shape):
+    """A broadcast dimension has stride 0: no single row stride reaches every
+    row, and one taken from the next dimension would lead past the storage."""
+    t = torch.zeros(base).expand(shape)
+
+    class T:
+        is_cuda, stride, is_contiguous = True, t.stride, t.is_contiguous
+    T.shape = t.shape
+    with pytest.raises(ValueError, match="rows must|contiguous"):
+        vq._rows(T(), "k", shape)
+
+
+def test_overlapping_rows_are_refused():
+    t = torch.zeros(4096).as_strided((3, 5, 2, 64), (5 * 64, 64, 64, 1))  # rows of 128, 64 apart
+
+    class T:
+        is_cuda, shape, stride, is_contiguous = True, t.shape, t.stride, t.is_contiguous
+    with pytest.raises(ValueError, match="share"):
+        vq._rows(T(), "k", (3, 5, 2, 64))
+
+
 def test_reference_attention():
     """Equal scores average the values; a one-hot score picks one; the mask is obeyed."""
     g = np.random.Generator(np.random.PCG64(1))
