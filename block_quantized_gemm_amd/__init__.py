@@ -182,7 +182,10 @@ class Workspace:
     The library leaves the counters at zero after every call, so it is zeroed
     once.  The zero fill runs on torch's current stream and is waited for here,
     so the buffer is ready for a call on any stream.  Calls sharing one
-    workspace must be ordered (one stream, or streams the caller orders)."""
+    workspace must be ordered (one stream, or streams the caller orders).  The
+    calls of several kernels that pass data through the buffer (greedy and tree
+    verification, tree attention) hold `lock` while they enqueue them, so that
+    host threads which share a workspace on one stream do not interleave."""
 
     def __init__(self, nbytes: int, device=None):
         torch = _torch()
@@ -192,6 +195,7 @@ class Workspace:
         if not torch.cuda.is_current_stream_capturing():
             alloc.synchronize()
         self._streams = {alloc.cuda_stream}
+        self.lock = threading.Lock()
 
     @property
     def nbytes(self) -> int:
@@ -235,6 +239,33 @@ def _workspace_args(workspace, kind: int, m: int, k: int, device, stream_handle:
             _auto_ws[key] = ws
         ws.used_on(stream_handle)
     return ws.ptr(), ws.nbytes
+
+
+_ws_needs = {}
+
+
+def _sized_workspace(query: str, sizes, workspace, device, stream_handle: int) -> Workspace:
+    """The workspace of a call that always needs one of `query`(*sizes) bytes:
+    the caller's, or ("auto") one cached per operator, device and stream and
+    grown to that.  The call enqueues its kernels under its lock."""
+    if workspace == "auto":
+        need = _ws_needs.get((query, sizes))
+        if need is None:
+            need = _ws_needs[(query, sizes)] = int(getattr(lib(), query)(*sizes))
+        key = (query, device, stream_handle)
+        ws = _auto_ws.get(key)
+        if ws is None or ws.nbytes < need:
+            with _auto_lock:
+                ws = _auto_ws.get(key)
+                if ws is None or ws.nbytes < need:
+                    ws = Workspace(need, device)
+                    _auto_ws[key] = ws
+    elif isinstance(workspace, Workspace):
+        ws = workspace
+    else:
+        raise TypeError("workspace must be a Workspace or 'auto'")
+    ws.used_on(stream_handle)
+    return ws
 
 
 def _kind(kind: str) -> int:
@@ -629,24 +660,13 @@ def greedy_verify(logits, draft, tokens_out=None, count_out=None, *, workspace="
         tokens_out = torch.empty(n, dtype=torch.int32, device=logits.device)
     if count_out is None:
         count_out = torch.empty(1, dtype=torch.int32, device=logits.device)
-    need = greedy_workspace_bytes(n, v)
     sh = _stream(stream)
-    if isinstance(workspace, Workspace):
-        ws = workspace
-    elif workspace == "auto":
-        key = ("greedy", str(logits.device), sh)
-        with _auto_lock:
-            ws = _auto_ws.get(key)
-            if ws is None or ws.nbytes < need:
-                ws = Workspace(need, logits.device)
-                _auto_ws[key] = ws
-    else:
-        raise TypeError("workspace must be a Workspace or 'auto'")
-    ws.used_on(sh)
+    ws = _sized_workspace("vq_greedy_workspace_bytes", (n, v), workspace, logits.device, sh)
     dptr = _dev_ptr(draft, "draft") if (draft is not None and draft.numel()) else None
-    st = lib().vq_greedy_verify(_dev_ptr(logits, "logits"), _dtype_code(logits), n, v, dptr,
-                                _dev_ptr(tokens_out, "tokens_out"), _dev_ptr(count_out, "count_out"),
-                                ws.ptr(), ws.nbytes, sh)
+    with ws.lock:
+        st = lib().vq_greedy_verify(_dev_ptr(logits, "logits"), _dtype_code(logits), n, v, dptr,
+                                    _dev_ptr(tokens_out, "tokens_out"), _dev_ptr(count_out, "count_out"),
+                                    ws.ptr(), ws.nbytes, sh)
     _check(st, "vq_greedy_verify")
     return tokens_out, count_out
 
@@ -708,33 +728,6 @@ def _like(t, stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
     with torch.cuda.stream(stream):
         return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-_ws_needs = {}
-
-
-def _sized_workspace(query: str, sizes, workspace, device, stream_handle: int):
-    """(pointer, bytes) of the workspace of a call that always needs one of
-    `query`(*sizes) bytes: the caller's Workspace, or ("auto") one cached per
-    operator, device and stream and grown to that."""
-    if workspace == "auto":
-        need = _ws_needs.get((query, sizes))
-        if need is None:
-            need = _ws_needs[(query, sizes)] = int(getattr(lib(), query)(*sizes))
-        key = (query, device, stream_handle)
-        ws = _auto_ws.get(key)
-        if ws is None or ws.nbytes < need:
-            with _auto_lock:
-                ws = _auto_ws.get(key)
-                if ws is None or ws.nbytes < need:
-                    ws = Workspace(need, device)
-                    _auto_ws[key] = ws
-    elif isinstance(workspace, Workspace):
-        ws = workspace
-    else:
-        raise TypeError("workspace must be a Workspace or 'auto'")
-    ws.used_on(stream_handle)
-    return ws.ptr(), ws.nbytes
 
 
 def _rows(t, name: str, shape) -> int:
@@ -818,13 +811,16 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, ctx_len, *, tree_mask=
     if out is None:
         out = _like(q, stream)
     sh, i32 = _raw_stream(stream), torch.int32
-    wp, wn = _sized_workspace("vq_tree_attention_workspace_bytes", (B, n, Hq, H, D), workspace, q.device, sh)
-    st = lib().vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
-                             _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                             _array(page_table, "page_table", (B, W), i32), _array(ctx_len, "ctx_len", (B,), i32),
-                             _array(tree_mask, "tree_mask", (B, n), torch.int64),
-                             _array(n_nodes, "n_nodes", (B,), i32), _array(out, "out", shape, dtype), B, n, Hq, H,
-                             D, page, P, W, D ** -0.5 if scale is None else scale, wp, wn, sh)
+    ws = _sized_workspace("vq_tree_attention_workspace_bytes", (B, n, Hq, H, D), workspace, q.device, sh)
+    with ws.lock:
+        st = lib().vq_tree_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(q),
+                                     _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+                                     _array(page_table, "page_table", (B, W), i32),
+                                     _array(ctx_len, "ctx_len", (B,), i32),
+                                     _array(tree_mask, "tree_mask", (B, n), torch.int64),
+                                     _array(n_nodes, "n_nodes", (B,), i32), _array(out, "out", shape, dtype), B, n,
+                                     Hq, H, D, page, P, W, D ** -0.5 if scale is None else scale, ws.ptr(), ws.nbytes,
+                                     sh)
     _check(st, "vq_tree_attention")
     return out
 
@@ -866,14 +862,16 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
     if count_out is None:
         count_out = _like(node_tokens[:, 0], stream)
     sh = _raw_stream(stream)
-    wp, wn = _sized_workspace("vq_tree_verify_workspace_bytes", (B, n, V), workspace, target.device, sh)
-    st = lib().vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
-                              _dtype_code(target), _array(node_tokens, "node_tokens", (B, n), i32),
-                              _array(parents, "parents", (B, n), i32), _array(n_nodes, "n_nodes", (B,), i32),
-                              _array(temperature, "temperature", (B,), f32),
-                              _array(uniforms, "uniforms", (B, n), f32), _array(noise, "noise", (B, V), f32),
-                              _array(tokens_out, "tokens_out", (B, n), i32), _array(path_out, "path_out", (B, n), i32),
-                              _array(count_out, "count_out", (B,), i32), B, n, V, wp, wn, sh)
+    ws = _sized_workspace("vq_tree_verify_workspace_bytes", (B, n, V), workspace, target.device, sh)
+    with ws.lock:
+        st = lib().vq_tree_verify(_dev_ptr(target, "target"), _array(draft, "draft", shape, target.dtype),
+                                  _dtype_code(target), _array(node_tokens, "node_tokens", (B, n), i32),
+                                  _array(parents, "parents", (B, n), i32), _array(n_nodes, "n_nodes", (B,), i32),
+                                  _array(temperature, "temperature", (B,), f32),
+                                  _array(uniforms, "uniforms", (B, n), f32), _array(noise, "noise", (B, V), f32),
+                                  _array(tokens_out, "tokens_out", (B, n), i32),
+                                  _array(path_out, "path_out", (B, n), i32),
+                                  _array(count_out, "count_out", (B,), i32), B, n, V, ws.ptr(), ws.nbytes, sh)
     _check(st, "vq_tree_verify")
     return tokens_out, path_out, count_out
 
