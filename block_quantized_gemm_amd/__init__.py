@@ -182,10 +182,12 @@ class Workspace:
     The library leaves the counters at zero after every call, so it is zeroed
     once.  The zero fill runs on torch's current stream and is waited for here,
     so the buffer is ready for a call on any stream.  Calls sharing one
-    workspace must be ordered (one stream, or streams the caller orders).  The
-    calls of several kernels that pass data through the buffer (greedy and tree
-    verification, tree attention) hold `lock` while they enqueue them, so that
-    host threads which share a workspace on one stream do not interleave."""
+    workspace must be ordered (one stream, or streams the caller orders), and
+    so must the replays of a graph captured with it (with "auto": the buffer of
+    the stream that the graph was captured on).  The calls of several kernels
+    that pass data through the buffer (greedy and tree verification, tree
+    attention) hold `lock` while they enqueue them, so that host threads which
+    share a workspace on one stream do not interleave."""
 
     def __init__(self, nbytes: int, device=None):
         torch = _torch()
@@ -215,7 +217,26 @@ class Workspace:
 
 
 _auto_ws = {}
+_outgrown_ws = []
 _auto_lock = threading.Lock()
+
+
+def _auto_workspace(key, need: int, device) -> Workspace:
+    """The cached workspace of `key`, replaced by a larger one when `need` is
+    more than it holds.  A replaced buffer is never given back: a HIP graph
+    captured with it writes to it at every replay, and other threads may be
+    about to use it.  Each is at least twice the one before, so that the
+    replaced ones together are no larger than the current one."""
+    ws = _auto_ws.get(key)
+    if ws is None or ws.nbytes < need:
+        with _auto_lock:
+            ws = _auto_ws.get(key)
+            if ws is None or ws.nbytes < need:
+                old, ws = ws, Workspace(need if ws is None else max(need, 2 * ws.nbytes), device)
+                if old is not None:
+                    _outgrown_ws.append(old)
+                _auto_ws[key] = ws
+    return ws
 
 
 def _workspace_args(workspace, kind: int, m: int, k: int, device, stream_handle: int):
@@ -231,13 +252,8 @@ def _workspace_args(workspace, kind: int, m: int, k: int, device, stream_handle:
     need = int(lib().vq_workspace_bytes(kind, m, k))
     if need == 0:
         return None, 0
-    key = (str(device), stream_handle)
-    with _auto_lock:
-        ws = _auto_ws.get(key)
-        if ws is None or ws.nbytes < need:
-            ws = Workspace(need, device)
-            _auto_ws[key] = ws
-        ws.used_on(stream_handle)
+    ws = _auto_workspace((str(device), stream_handle), need, device)
+    ws.used_on(stream_handle)
     return ws.ptr(), ws.nbytes
 
 
@@ -252,14 +268,7 @@ def _sized_workspace(query: str, sizes, workspace, device, stream_handle: int) -
         need = _ws_needs.get((query, sizes))
         if need is None:
             need = _ws_needs[(query, sizes)] = int(getattr(lib(), query)(*sizes))
-        key = (query, device, stream_handle)
-        ws = _auto_ws.get(key)
-        if ws is None or ws.nbytes < need:
-            with _auto_lock:
-                ws = _auto_ws.get(key)
-                if ws is None or ws.nbytes < need:
-                    ws = Workspace(need, device)
-                    _auto_ws[key] = ws
+        ws = _auto_workspace((query, device, stream_handle), need, device)
     elif isinstance(workspace, Workspace):
         ws = workspace
     else:

@@ -1,7 +1,9 @@
 """The binding's cached workspaces on the host: a stand-in for the library
 records which buffer each call was given and when."""
+import gc
 import threading
 import time
+import weakref
 
 import pytest
 import torch
@@ -41,7 +43,7 @@ class Lib:
     patience = 0.0
 
     def __getattr__(self, name):
-        if name.endswith("workspace_bytes"):
+        if "workspace_bytes" in name:
             return lambda *sizes: self.need
         return lambda *args: self._call(args[-3])  # workspace, bytes, stream end every list
 
@@ -89,3 +91,36 @@ def test_threads_on_one_stream_do_not_interleave(fake, call):
     for t in threads:
         t.join()
     assert len(fake.seen) == 2 and not fake.shared
+
+
+@pytest.mark.parametrize("call", [_attention, _tree, _greedy])
+def test_a_replaced_buffer_is_kept(fake, call):
+    """A graph captured with the cached buffer has its address in its nodes:
+    when a later call needs a larger one, the memory must not be handed out
+    again.  What is kept stays below what is in use."""
+    call()
+    first = weakref.ref(next(iter(vq._auto_ws.values())).tensor)
+    sizes, held = [], []
+    for need in range(1025, 40000, 1000):
+        fake.need = need
+        vq._ws_needs.clear()
+        call()
+        ws = next(iter(vq._auto_ws.values()))
+        assert ws.nbytes >= need
+        if ws.nbytes not in sizes:
+            sizes.append(ws.nbytes)
+            held.append(ws.ptr())
+    gc.collect()
+    assert first() is not None and len(set(held)) == len(held)
+    assert len(sizes) > 2 and 1024 + sum(sizes[:-1]) <= sizes[-1]
+    assert set(held) <= set(fake.seen)
+
+
+def test_a_replaced_buffer_of_the_verify_gemms_is_kept(fake):
+    """The same for the workspace that the verify GEMMs share per stream."""
+    vq._workspace_args("auto", vq.KIND_Q4_0, 256, 256, torch.device("cpu"), STREAM)
+    first = weakref.ref(next(iter(vq._auto_ws.values())).tensor)
+    fake.need = 5000
+    ptr, nbytes = vq._workspace_args("auto", vq.KIND_Q4_0, 512, 256, torch.device("cpu"), STREAM)
+    gc.collect()
+    assert nbytes >= 5000 and first() is not None and first().data_ptr() != ptr
