@@ -241,7 +241,9 @@ struct Wave {
         for (int x = 1; x < 8; ++x)
             top = fmaxf(top, s[x]);
         if (__any(top > acc.m[qt] + kSlack)) {
-            const float m_new = fmaxf(acc.m[qt], row_max(top));
+            // row by row: a row keeps its maximum, and with it the rounding of
+            // its probabilities, when only its neighbours exceed theirs
+            const float most = row_max(top), m_new = most > acc.m[qt] + kSlack ? most : acc.m[qt];
             const float shrink = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(acc.m[qt] - m_new);
             acc.m[qt] = m_new;
             acc.l[qt] *= shrink;
