@@ -3,8 +3,8 @@
 // For each query row (node i of sequence b, query head h):
 //   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),  s_t = scale * (q . k_t),
 // over the cached positions t < ctx_len[b] and the nodes its mask names, in
-// one pass with a running maximum m and sum l: when m grows, what was summed
-// is multiplied by exp(m_old - m_new).
+// one pass with a base m that follows the running maximum, and a sum l: when m
+// grows, what was summed is multiplied by exp(m_old - m_new).
 //
 // The rows of one sequence that share a key/value head (nodes x query heads of
 // the head's group) are the 16 columns of MFMA tiles, 32 tokens a step:
@@ -55,11 +55,19 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;         // tokens per step
 constexpr int kMinSteps = 4;      // steps per range at least: one per wave
-// The running maximum is only raised when a score exceeds it by more than
-// this (in powers of two): until then probabilities grow to 2^8 at most, which
-// costs no accuracy in fp32 sums or in 16-bit floating-point operands, and the
-// reduction over the row's four lanes and the scaling of O are skipped.
+// Probabilities are exp2(s - base).  The base is only raised when a score
+// exceeds the row's maximum when it was set by more than this (in powers of
+// two): until then the reduction over the row's four lanes and the scaling of O
+// are skipped.
 constexpr float kSlack = 8.f;
+// The base lies this far below that maximum.  bf16 has fp32's exponents and
+// needs none.  The probabilities that the second product takes in fp16 lose
+// bits below 2^-14 and vanish below 2^-25, while their sum l, in fp32, keeps
+// them: at base = maximum, 128k tokens that each hold 2^-25 of it drop 0.4% of
+// the weight from O alone.  2^7 higher the largest is 2^(8 + 7), below fp16's
+// 65504, and bits are lost only below 2^-21 of the maximum.
+template <int DT>
+constexpr float kLift = DT == VQ_DTYPE_F16 ? 7.f : 0.f;
 
 struct KArgs {
     const uint16_t *q, *k, *v, *k_cache, *v_cache;
@@ -160,8 +168,8 @@ __device__ __forceinline__ float norm_of(float l, int ctx, uint64_t seen) {
 }
 
 // One wave's state over a (sequence, head) pair: D / 16 channel tiles of O^T
-// for QT tiles of 16 rows, and each row's maximum (in powers of two, equal in
-// its four lanes) and this lane's part of its sum.
+// for QT tiles of 16 rows, and each row's base (in powers of two, equal in its
+// four lanes) and this lane's part of its sum.
 template <int D, int QT>
 struct Acc {
     f32x4 o[QT][D / 16];
@@ -233,17 +241,18 @@ struct Wave {
     }
 
     // Folds eight scores of each lane's row (already in powers of two, -inf
-    // where unseen) into the running maximum and sum; returns the
-    // probabilities in the values' type.
+    // where unseen) into the base and sum; returns the probabilities in the
+    // values' type, the operand type of the second product.
     __device__ __forceinline__ u32x4 fold(const float (&s)[8], int qt, Acc<D, QT> &acc) const {
         float top = s[0];
 #pragma unroll
         for (int x = 1; x < 8; ++x)
             top = fmaxf(top, s[x]);
-        if (__any(top > acc.m[qt] + kSlack)) {
-            // row by row: a row keeps its maximum, and with it the rounding of
+        constexpr float kRoom = kLift<DT> + kSlack;
+        if (__any(top > acc.m[qt] + kRoom)) {
+            // row by row: a row keeps its base, and with it the rounding of
             // its probabilities, when only its neighbours exceed theirs
-            const float most = row_max(top), m_new = most > acc.m[qt] + kSlack ? most : acc.m[qt];
+            const float most = row_max(top), m_new = most > acc.m[qt] + kRoom ? most - kLift<DT> : acc.m[qt];
             const float shrink = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(acc.m[qt] - m_new);
             acc.m[qt] = m_new;
             acc.l[qt] *= shrink;

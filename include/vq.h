@@ -530,7 +530,8 @@ size_t vq_greedy_workspace_bytes(int64_t n_rows, int64_t vocab);
  *             (VQ_ERR_WORKSPACE if NULL or smaller); calls that share one must
  *             not overlap in time.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded
- * to dtype for the product with the values.  Results are the same bits from
+ * to dtype for the product with the values (F16: with all bits down to 2^-21 of
+ * the row's largest, within 2^-32 of it below).  Results are the same bits from
  * run to run; where a long context is cut between workgroups follows the
  * whole call (all sequences' lengths) and the device's CU count.
  */
