@@ -139,7 +139,7 @@ int64_t groups_of(int64_t items, int64_t batch) { return (std::max(items, batch)
 }  // namespace
 
 bool kv_append_fits(int64_t n_layers, int64_t batch, int64_t n, int64_t kv_heads, int64_t head_dim) {
-    return groups_of(items_of(n_layers, batch, n, kv_heads, head_dim), batch) <= 0x7FFFFFFF;
+    return groups_of(items_of(n_layers, batch, n, kv_heads, head_dim), batch) * kThreads <= 0xFFFFFFFFll;
 }
 
 hipError_t launch_kv_append(const KvAppendArgs &p) {

@@ -59,7 +59,8 @@ struct KvAppendArgs {
     hipStream_t stream;
 };
 hipError_t launch_kv_append(const KvAppendArgs &a);
-// Whether one launch can cover this many rows (the grid holds 2^31 - 1 workgroups).
+// Whether one launch can cover this many rows (a grid dimension holds 2^32 - 1
+// threads, and a launch past that is refused only when it is made).
 bool kv_append_fits(int64_t n_layers, int64_t batch, int64_t n, int64_t kv_heads, int64_t head_dim);
 
 }  // namespace vq

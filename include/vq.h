@@ -614,7 +614,9 @@ size_t vq_tree_verify_workspace_bytes(int64_t batch, int64_t n, int64_t vocab);
  *             page_size
  * Every destination is written by one row only as long as no page belongs to
  * two sequences.  Sizes: 1 <= n_layers <= VQ_MAX_HEADS, 1 <= n <= VQ_MAX_DIM,
- * and all rows together within one launch (about 2^45 elements of keys).
+ * and all rows together within one launch: n_layers * batch * ((n + 30) / 32 + 1)
+ * * kv_heads * head_dim / 2 below 2^32 (blocks of 32 positions, 64 elements of
+ * keys and of values a thread).
  */
 int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype,
                  void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *ctx_len,

@@ -75,6 +75,22 @@ def test_append_refusals():
         assert _append(**bad) == vq.VQ_ERR_BAD_SHAPE, bad
 
 
+def test_append_refuses_what_no_launch_holds():
+    """A thread writes 8 positions x 8 channels, and a grid dimension holds
+    2^32 - 1 threads: more is refused as a size, before anything is enqueued."""
+    for ok, sizes in ((True, dict(layers=1024, b=4096, n=1, h=15, d=128)), (False, dict(layers=1024, b=4096, n=1, h=16, d=128)),
+                      (False, dict(layers=1024, b=4096, n=1, h=64, d=128)), (False, dict(layers=1, b=64, n=1 << 24, h=4, d=64)),
+                      (True, dict(layers=1, b=63, n=1 << 24, h=4, d=64)), (False, dict(layers=1024, b=2048, n=33, h=16, d=128))):
+        blocks = (sizes["n"] + 30) // 32 + 1
+        threads = sizes["layers"] * sizes["b"] * blocks * sizes["h"] * sizes["d"] // 2
+        assert (threads < 1 << 32) == ok
+        if not ok:
+            width = sizes["h"] * sizes["d"]
+            assert _append(ks=width, vs=width, **sizes) == vq.VQ_ERR_BAD_SHAPE, sizes
+        elif not torch.cuda.is_available():  # past the size checks
+            assert _append(ks=sizes["h"] * sizes["d"], vs=sizes["h"] * sizes["d"], **sizes) == vq.VQ_ERR_DEVICE, sizes
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="without a device every valid call is refused")
 def test_no_device_is_an_error():
     assert _attn() == vq.VQ_ERR_DEVICE and _verify() == vq.VQ_ERR_DEVICE and _append() == vq.VQ_ERR_DEVICE
