@@ -15,9 +15,11 @@
 // elements cost one per token and channel.
 //
 // Measured (8 heads of 128, one MI355X): two prompts of 8,190 rows into one
-// layer 32.7 us (134 MB moved, 4.1 TB/s), bound by the bytes; 32 paths of 1 to 8
-// rows into 16 layers 27.8 us (52 us with element stores), bound by the value
-// blocks' lines, of which a few rows fill a part; one path into 16 layers
+// layer 32 to 33 us (134 MB moved, 4.1 TB/s), bound by the bytes; 32 paths of 1
+// to 8 rows into 16 layers 26 to 27.5 us (52 us with element stores), bound by
+// the value blocks' lines, of which a few rows fill a part: 50 MB are read and
+// 690,000 lines' parts written (a quarter of them 64 whole bytes) for rows of
+// 10.7 MB; one path into 16 layers
 // 4.9 us in the kernel, three dependent memory round trips (lengths and path,
 // page, rows).  Keys and values in one thread took 43 us on the prompts: their
 // 300 registers left one wave per SIMD.

@@ -26,22 +26,29 @@
 // boundary leaves its pieces (m, l, O in fp32) in the workspace, and a second
 // kernel joins them in order.
 //
-// Measured on one MI355X (whole call, bf16 unless noted; bytes = the cached
-// keys and values once):
-//   1 sequence, 8-node chain, 509 tokens, 64 / 8 heads of 128     22.9 us
-//   32 sequences, single tokens, up to 4k, 32 / 8 of 64, f16      47.1 us  2.9 TB/s
-//   8 sequences, 16-node trees, up to 16k, 64 / 8 of 128         142.5 us  2.3 TB/s
-//   1 sequence, 16-node tree, 128k, 64 / 8 of 128                210.7 us  2.6 TB/s
-//   4 sequences, 61-node trees, up to 8k, 32 / 4 of 256, f16     254.9 us
+// Measured on one MI355X (whole call, bf16 unless noted; the rate is the cached
+// keys and values, once, over that time), and each kernel's median in a trace,
+// whose own overhead is in it:
+//                                                              call            main    join
+//   1 sequence, 8-node chain, 509 tokens, 64 / 8 heads of 128   23 us           18.4    4.5
+//   32 sequences, single tokens, up to 4k, 32 / 8 of 64, f16    46 to 49        41.0    5.4   2.9 TB/s
+//   8 sequences, 16-node trees, up to 16k, 64 / 8 of 128       144             142.1   10.8   2.3 TB/s
+//   1 sequence, 16-node tree, 128k, 64 / 8 of 128              211             214.5    9.2   2.5 TB/s
+//   4 sequences, 61-node trees, up to 8k, 32 / 4 of 256, f16   255 to 260      246.7    9.4
 // What bounds them: with more rows than a workgroup holds (32, or 16 at D =
-// 256) every group of rows reads the keys and values again, so the 128-row
-// calls move four times the bytes, 10 TB/s out of L2 and the Infinity Cache;
-// the 61-node call reads them 31 times.  Few rows: the page number of a step is
-// read by a vector load and waited for, which also waits for the step's
-// operands already on their way, so a wave has one step in flight; then the
-// start (3 to 4 us: the scan, the first page and operands) and the joining
-// kernel (5 us small, 10 us large).  The short call is the two kernels' 9 us
-// and the host's time to make the call.
+// 256) every group of rows reads the keys and values again.  L2 answers 1.25 GB
+// of requests for the 8 trees and 2.18 GB for the 128k tree (four times the
+// bytes; 9 and 10 TB/s) and sends 0.40 and 0.58 GB of them to memory; for the
+// 61-node trees 2.0 to 2.4 GB (once per 16 rows; 8.5 TB/s) and 0.18 GB, and that
+// kernel spills 51 registers.  The matrix units are busy 15% of the 128k call.
+// Few rows: the page number of a step is read by a vector load and waited for,
+// which also waits for the step's operands already on their way, so a wave has
+// one step in flight.  The short chain is bound by the main kernel, not by its
+// bytes (2.4 MB) nor by the host, since the two kernels fill the call: 68
+// workgroups, each a chain of dependent steps (the scan, page numbers, operands,
+// four-wave join), and the ranges that hold the end of one head and the start
+// of the next go through two such chains.  Where in the chain the time goes has
+// not been measured.
 #include <atomic>
 
 #include "tree_internal.h"
@@ -659,11 +666,12 @@ __global__ __launch_bounds__(kThreads) void tree_join_kernel(KArgs a) {
 
 constexpr int kMaxWorkgroups = 1024;
 
-// Tiles of 16 query rows per wave: as many as the rows need, up to what 256
-// registers hold beside a step of keys and values (two tiles of D = 128: 64 for
-// O, 64 for the operands, 32 for the scores and probabilities; D = 256 needs 64
-// and 128 for one).  Four tiles would halve the re-reading of 128-row calls and
-// do not fit.
+// Tiles of 16 query rows per wave, all four waves of a workgroup holding the
+// same rows: as many as the rows need, up to what a wave's 256 registers hold
+// beside a step of keys and values (two tiles of D = 128: 64 for O, 64 for the
+// operands, 32 for the scores and probabilities; D = 256 needs 64 and 128 for
+// one, and spills 51 as it is).  More rows per workgroup, and so less
+// re-reading, would take waves with different rows.
 int row_tiles(int rows, int D) {
     const int most = D == 256 ? 1 : 2;
     return rows <= 16 ? 1 : most;

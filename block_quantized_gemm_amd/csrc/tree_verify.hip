@@ -19,13 +19,16 @@
 // another pass over that node's two rows.  The third draws the last token,
 // the row split over many workgroups; the last to arrive writes it.
 //
-// Measured on one MI355X (whole call; the kernels' own times in order):
-//   1 chain of 16, 151,936 bf16 logits, drawn children    20.0 us (5.1 + 5.2 + 6.7)
-//   4 trees of up to 61, 32,001 fp32 logits, given         22.9 us (7.6 + 9.8 + 7.0)
-//   32 trees of up to 16, 151,936 bf16 logits, drawn      109.5 us (45.8 + 61.6 + 11.1)
-// The first kernel is bound by reading the rows (the large batch's at about
-// 4 TB/s), small calls by the three kernels' start and their chains of
-// dependent loads.  A retry's pass over two rows is the work of one workgroup:
+// Measured on one MI355X: the whole call, and each kernel's median in a trace,
+// whose own overhead is in it:
+//                                                           call          stats   walk   draw
+//   1 chain of 16, 151,936 bf16 logits, drawn children      19 to 20 us     5.2    5.5    6.7
+//   4 trees of up to 61, 32,001 fp32 logits, given          23 to 25        7.4    9.8    6.8
+//   32 trees of up to 16, 151,936 bf16 logits, drawn        98 to 112      45.3   61.5   11.1
+// The first kernel is bound by reading the rows (175 MB of the large batch's,
+// 3.9 TB/s), small calls by the three kernels' start and their chains of
+// dependent loads, the smallest by the host's three launches (19 us from
+// Python).  A retry's pass over two rows is the work of one workgroup:
 // 152k tokens cost it two exponentials each, about 20 us of one CU, and the walk
 // lasts as long as its unluckiest sequence.
 #include "tree_internal.h"
