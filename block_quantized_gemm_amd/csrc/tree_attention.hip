@@ -256,10 +256,12 @@ struct Wave {
         for (int x = 1; x < 8; ++x)
             top = fmaxf(top, s[x]);
         constexpr float kRoom = kLift<DT> + kSlack;
-        if (__any(top > acc.m[qt] + kRoom)) {
+        // by the difference, which is the probabilities' exponent to the bit: a
+        // sum rounds where neighbouring floats are more than 1 apart
+        if (__any(top - acc.m[qt] > kRoom)) {
             // row by row: a row keeps its base, and with it the rounding of
             // its probabilities, when only its neighbours exceed theirs
-            const float most = row_max(top), m_new = most > acc.m[qt] + kRoom ? most - kLift<DT> : acc.m[qt];
+            const float most = row_max(top), m_new = most - acc.m[qt] > kRoom ? most - kLift<DT> : acc.m[qt];
             const float shrink = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(acc.m[qt] - m_new);
             acc.m[qt] = m_new;
             acc.l[qt] *= shrink;

@@ -60,3 +60,26 @@ def test_probabilities_at_the_head_room_stay_finite():
     got = c.run()
     assert torch.isfinite(got).all()
     c.check(got)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_past_2_24(D):
+    """Scores so large that neighbouring fp32 values are 2 apart: the choice to
+    raise the base, and with it the bound on fp16 probabilities, must hold for
+    the difference of two scores and not for a rounded sum.  Positions alternate
+    by 128 between scores of s and s + 8 (in powers of two, s = 1.5 * 2^24), so
+    that a wave meets both; values 1 and 2."""
+    n, L = 64, 2048
+    c = Case(802, "f16", n, 64, 1, D, 64, [L], mask=None)
+    c.scale = 0.6931471824645996  # times log2 e = 1 in fp32
+    c.q[...] = 0
+    c.q[..., 0], c.q[..., 1] = 6144.0, 1.0
+    c.k[...] = 0
+    for page in range(L // 64):
+        at, high = int(c.table[0, page]), page // 2 % 2
+        c.k_cache[at], c.v_cache[at] = 0, 1.0 + high
+        c.k_cache[at, ..., 0], c.k_cache[at, ..., 1] = 4096.0, 8.0 * high
+    want = (1 + 2 * 256) / (1 + 256)
+    got = c.run().to(torch.float64).numpy()
+    # one rounding of the probabilities' weights (exact powers of two here) and one of the output
+    assert np.abs(got / want - 1).max() <= 2 * UNIT["f16"], (got.min(), got.max(), want)
