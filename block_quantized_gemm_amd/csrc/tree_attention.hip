@@ -31,10 +31,10 @@
 // whose own overhead is in it:
 //                                                              call            main    join
 //   1 sequence, 8-node chain, 509 tokens, 64 / 8 heads of 128   23 us           18.4    4.5
-//   32 sequences, single tokens, up to 4k, 32 / 8 of 64, f16    46 to 49        41.0    5.4   2.9 TB/s
+//   32 sequences, single tokens, up to 4k, 32 / 8 of 64, f16    45 to 49        41.0    5.4   2.9 TB/s
 //   8 sequences, 16-node trees, up to 16k, 64 / 8 of 128       144             142.1   10.8   2.3 TB/s
 //   1 sequence, 16-node tree, 128k, 64 / 8 of 128              211             214.5    9.2   2.5 TB/s
-//   4 sequences, 61-node trees, up to 8k, 32 / 4 of 256, f16   255 to 260      246.7    9.4
+//   4 sequences, 61-node trees, up to 8k, 32 / 4 of 256, f16   252 to 260      246.7    9.4
 // What bounds them: with more rows than a workgroup holds (32, or 16 at D =
 // 256) every group of rows reads the keys and values again.  L2 answers 1.25 GB
 // of requests for the 8 trees and 2.18 GB for the 128k tree (four times the
