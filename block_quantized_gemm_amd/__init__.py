@@ -775,6 +775,14 @@ def _array(t, name: str, shape, dtype):
     raise ValueError("%s must be a contiguous device tensor, %s %s" % (name, dtype, tuple(shape)))
 
 
+def _not_in_place(out, name: str, **inputs):
+    """Refuses an output that is one of the call's inputs: workgroups read the
+    input while others already write the output."""
+    for other, t in inputs.items():
+        if t is not None and t.data_ptr() == out.data_ptr():
+            raise ValueError("%s must not be %s: the call reads it while it writes" % (name, other))
+
+
 def _cache(k_cache, v_cache, lead, dtype):
     """(n_pages, kv_heads, page_size, head_dim) of a pair of caches with leading dimensions `lead`."""
     shape = k_cache.shape
@@ -856,7 +864,8 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
     variates; parents: int32 [B][n] (None: a chain); n_nodes: int32 [B] (None:
     n); temperature: float32 [B] (None: 1; 0: greedy).  Returns (tokens
     int32 [B][n], path int32 [B][n], count int32 [B]): the committed tokens,
-    the nodes they follow, and how many there are."""
+    the nodes they follow, and how many there are; the outputs may be given,
+    in memory that is none of the inputs'."""
     torch = _torch()
     if target.dim() != 3:
         raise ValueError("target must be [batch][n][vocab]")
@@ -866,10 +875,16 @@ def tree_verify(target, draft, node_tokens, uniforms, noise, *, parents=None, n_
         raise ValueError("node_tokens must be [batch][n]")
     if tokens_out is None:
         tokens_out = _like(node_tokens, stream)
+    else:
+        _not_in_place(tokens_out, "tokens_out", node_tokens=node_tokens, parents=parents)
     if path_out is None:
         path_out = _like(node_tokens, stream)
+    else:
+        _not_in_place(path_out, "path_out", node_tokens=node_tokens, parents=parents, tokens_out=tokens_out)
     if count_out is None:
         count_out = _like(node_tokens[:, 0], stream)
+    else:
+        _not_in_place(count_out, "count_out", n_nodes=n_nodes)
     sh = _raw_stream(stream)
     ws = _sized_workspace("vq_tree_verify_workspace_bytes", (B, n, V), workspace, target.device, sh)
     with ws.lock:
@@ -892,7 +907,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
     k, v: float16 / bfloat16 [B][n][H][D] with caches as for tree_attention, or
     [L][B][n][H][D] with caches [L][P]... of L layers; path: int32 [B][n];
     count: int32 [B], as tree_verify returns them.  Returns the new lengths,
-    int32 [B]."""
+    int32 [B] (len_out when given, which must not be ctx_len or count: the call
+    reads them while it writes)."""
     torch = _torch()
     if k.dim() not in (4, 5):
         raise ValueError("k must be [n_layers][batch][n][kv_heads][head_dim] or without the layers")
@@ -909,6 +925,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
     W, i32 = page_table.shape[1], torch.int32
     if len_out is None:
         len_out = _like(ctx_len, stream)
+    else:
+        _not_in_place(len_out, "len_out", ctx_len=ctx_len, count=count)
     st = lib().vq_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _dev_ptr(k_cache, "k_cache"),
                             _dev_ptr(v_cache, "v_cache"), _array(page_table, "page_table", (B, W), i32),
                             _array(ctx_len, "ctx_len", (B,), i32), _array(path, "path", (B, n), i32),

@@ -74,6 +74,29 @@ def _tree():
                    torch.ones(1, 8))
 
 
+@pytest.mark.parametrize("kw", ["ctx_len", "count"])
+def test_append_in_place_lengths_are_refused(fake, kw):
+    """Lengths updated in place would be read by some workgroups after others
+    have written them."""
+    k = torch.zeros(2, 2, 2, 64, dtype=torch.float16)
+    lens, count = torch.zeros(2, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="len_out must not be " + kw):
+        vq.kv_append(k, k, torch.zeros(2, 2, 32, 64, dtype=torch.float16),
+                     torch.zeros(2, 2, 1, 64, 32, dtype=torch.float16), torch.zeros(2, 1, dtype=torch.int32), lens,
+                     count=count, len_out=lens if kw == "ctx_len" else count)
+    assert not fake.seen
+
+
+def test_verify_in_place_outputs_are_refused(fake):
+    target, tokens, u, e = torch.zeros(1, 2, 8), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, 2), torch.ones(1, 8)
+    nodes, parents = torch.ones(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
+    for kw in (dict(tokens_out=tokens), dict(path_out=tokens), dict(path_out=parents), dict(tokens_out=parents),
+               dict(count_out=nodes)):
+        with pytest.raises(ValueError, match="must not be"):
+            vq.tree_verify(target, None, tokens, u, e, parents=parents, n_nodes=nodes, **kw)
+    assert not fake.seen
+
+
 def _greedy():
     vq.greedy_verify(torch.zeros(2, 8), torch.zeros(1, dtype=torch.int32))
 
