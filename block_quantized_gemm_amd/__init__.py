@@ -90,9 +90,19 @@ SIGNATURES = {
     "vq_tree_verify_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "vq_kv_append": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                           _I64, _I64, _P]),
+    "vq_gemm_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
+    "vq_gated_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
+    "vq_w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "vq_gated_w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "vq_residual_norm": (_I, [_P, _I, _P, _I, _P, _P, _I, _F, _P, _F, _P, _P, _I, _P, _I64, _I64, _P]),
+    "vq_quant_rows_int8": (_I, [_P, _I, _P, _P, _I64, _I64, _P]),
+    "vq_rotate": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I,
+                       _F, _P]),
     "vq_status_string": (ctypes.c_char_p, [_I]),
     "vq_version": (_I, []),
 }
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -934,3 +944,251 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
                             lead[0] if lead else 1, B, n, H, D, page, P, W, _raw_stream(stream))
     _check(st, "vq_kv_append")
     return len_out
+
+
+# ---------------------------------------------------------------- the rest of a decoder layer
+
+def _here(*tensors):
+    """Refuses tensors of another device than the current one: the call's
+    kernels run there."""
+    dev = _torch()._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on the current device, cuda:%d" % dev)
+
+
+def _span(t):
+    """First and one past the last byte of a tensor's elements."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + last * t.element_size()
+
+
+def _apart(out, name: str, **inputs):
+    """Refuses an output that shares memory with another argument."""
+    lo, hi = _span(out)
+    for other, t in inputs.items():
+        if t is not None:
+            a, b = _span(t)
+            if a < hi and lo < b:
+                raise ValueError("%s must not share memory with %s" % (name, other))
+
+
+def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", stream=None):
+    """out[N][M] = x_scales[n] * w_scales[m] * (x[N][K] @ w[M][K]^T) + bias[m].
+
+    w: int8 [M][K]; w_scales: float32 [M]; x: int8 [N][K] and x_scales: float32
+    [N], as quant_rows_int8 and residual_norm write them; bias: float32 [M] or
+    None; out: float16 / bfloat16 / float32 [N][M].  The integer sums are exact:
+    a row's bits do not depend on the other rows.  workspace: "auto" (a cached
+    one per device and stream), a Workspace, or None (a slower form, the same
+    bits)."""
+    torch = _torch()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [N][K] and w [M][K]")
+    N, K = x.shape
+    M = w.shape[0]
+    i8, f32 = torch.int8, torch.float32
+    _check_2d(out, "out", (N, M))
+    _here(w, w_scales, x, x_scales, bias, out)
+    _apart(out, "out", w=w, w_scales=w_scales, x=x, x_scales=x_scales, bias=bias)
+    sh = _raw_stream(stream)
+    wp, wn = _w8a8_workspace("vq_w8a8_workspace_bytes", M, K, workspace, x.device, sh)
+    st = lib().vq_gemm_w8a8(_array(w, "w", (M, K), i8), _array(w_scales, "w_scales", (M,), f32),
+                            _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
+                            _array(bias, "bias", (M,), f32), _dev_ptr(out, "out"), _dtype_code(out), N, M, K, wp, wn,
+                            sh)
+    _check(st, "vq_gemm_w8a8")
+    return out
+
+
+def _w8a8_workspace(query, m, k, workspace, device, stream_handle):
+    """(pointer, bytes) for a product of 8-bit codes."""
+    if workspace is None:
+        return None, 0
+    ws = _sized_workspace(query, (m, k), workspace, device, stream_handle)
+    return ws.ptr(), ws.nbytes
+
+
+def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activation: str = "silu", workspace="auto",
+               stream=None):
+    """out[N][F] = act(x @ w_gate^T) * (x @ w_up^T), both factors as gemm_w8a8
+    forms them (no bias), in one pass over the weights.
+
+    w_gate, w_up: int8 [F][K] (they may be the halves of one [2 F][K] matrix)
+    with scales float32 [F]; x, x_scales, out, workspace: as for gemm_w8a8;
+    activation: "silu", "gelu" or "gelu_tanh"."""
+    torch = _torch()
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % sorted(ACTIVATIONS))
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x must be [N][K] and w_gate [F][K]")
+    N, K = x.shape
+    F = w_gate.shape[0]
+    i8, f32 = torch.int8, torch.float32
+    _check_2d(out, "out", (N, F))
+    _here(w_gate, gate_scales, w_up, up_scales, x, x_scales, out)
+    _apart(out, "out", w_gate=w_gate, gate_scales=gate_scales, w_up=w_up, up_scales=up_scales, x=x,
+           x_scales=x_scales)
+    sh = _raw_stream(stream)
+    wp, wn = _w8a8_workspace("vq_gated_w8a8_workspace_bytes", F, K, workspace, x.device, sh)
+    st = lib().vq_gated_w8a8(_array(w_gate, "w_gate", (F, K), i8), _array(gate_scales, "gate_scales", (F,), f32),
+                             _array(w_up, "w_up", (F, K), i8), _array(up_scales, "up_scales", (F,), f32),
+                             _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
+                             ACTIVATIONS[activation], _dev_ptr(out, "out"), _dtype_code(out), N, F, K, wp, wn, sh)
+    _check(st, "vq_gated_w8a8")
+    return out
+
+
+def w8a8_workspace_bytes(m: int, k: int) -> int:
+    """Workspace bytes of gemm_w8a8 for any number of rows."""
+    return int(lib().vq_w8a8_workspace_bytes(m, k))
+
+
+def gated_w8a8_workspace_bytes(f: int, k: int) -> int:
+    """Workspace bytes of gated_w8a8 for any number of rows."""
+    return int(lib().vq_gated_w8a8_workspace_bytes(f, k))
+
+
+def residual_norm(residual, y=None, weight=None, *, out, scales_out=None, residual_out=None, post_weight=None,
+                  gate=None, alpha: float = 1.0, eps: float = 1e-6, stream=None):
+    """The residual update behind one block and the norm before the next:
+
+        u = y, or y / sqrt(mean(y^2) + eps) * post_weight
+        x = residual + alpha * gate * u                    -> residual_out
+        out = x / sqrt(mean(x^2) + eps) * weight
+
+    residual: float16 / bfloat16 / float32 [N][C]; y: float16 / bfloat16 [N][C]
+    or None (x = residual); weight, post_weight: float32 [C] or None (1); gate:
+    float32 [C], or [N][C] of y's dtype, or None (1); residual_out: like
+    residual (residual itself for an update in place), or None: not written;
+    out: float16 / bfloat16 [N][C], or int8 with scales_out float32 [N]: codes
+    and scales as quant_rows_int8 forms them.  Returns out, or (out,
+    scales_out) for int8."""
+    torch = _torch()
+    if residual.dim() != 2:
+        raise ValueError("residual must be [N][C]")
+    shape = N, C = tuple(residual.shape)
+    f32 = torch.float32
+    if y is None and (post_weight is not None or gate is not None or residual_out is not None):
+        raise ValueError("post_weight, gate and residual_out go with y")
+    if (out.dtype == torch.int8) != (scales_out is not None):
+        raise ValueError("scales_out goes with an int8 out")
+    if y is not None and y.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("y must be float16 or bfloat16")
+    gate_rows = gate is not None and gate.dim() == 2
+    ydt = None if y is None else y.dtype
+    _here(residual, y, weight, out, scales_out, residual_out, post_weight, gate)
+    rest = dict(weight=weight, post_weight=post_weight, gate=gate, y=y)
+    _apart(out, "out", residual=residual, residual_out=residual_out, scales_out=scales_out, **rest)
+    if scales_out is not None:
+        _apart(scales_out, "scales_out", residual=residual, residual_out=residual_out, **rest)
+    if residual_out is not None:
+        same = residual_out.data_ptr() == residual.data_ptr()
+        _apart(residual_out, "residual_out", residual=None if same else residual, **rest)
+    st = lib().vq_residual_norm(
+        _array(residual, "residual", shape, residual.dtype), _dtype_code(residual), _array(y, "y", shape, ydt),
+        0 if y is None else _dtype_code(y), _array(post_weight, "post_weight", (C,), f32),
+        _array(gate, "gate", shape if gate_rows else (C,), ydt if gate_rows else f32), int(gate_rows), alpha,
+        _array(weight, "weight", (C,), f32), eps, _array(residual_out, "residual_out", shape, residual.dtype),
+        _array(out, "out", shape, out.dtype), _dtype_code(out), _array(scales_out, "scales_out", (N,), f32), N, C,
+        _raw_stream(stream))
+    _check(st, "vq_residual_norm")
+    return out if scales_out is None else (out, scales_out)
+
+
+def quant_rows_int8(x, q_out, scales_out, *, stream=None):
+    """Per row: s = amax / 127 (fp32), q = clamp(rint(x / s), +-127).
+
+    x: float16 / bfloat16 / float32 [N][K]; q_out: int8 [N][K]; scales_out:
+    float32 [N].  A row with a NaN or an infinity gets the scale NaN and codes
+    0."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [N][K]")
+    N, K = x.shape
+    _here(x, q_out, scales_out)
+    _apart(q_out, "q_out", x=x, scales_out=scales_out)
+    _apart(scales_out, "scales_out", x=x)
+    st = lib().vq_quant_rows_int8(_dev_ptr(x, "x"), _dtype_code(x), _array(q_out, "q_out", (N, K), torch.int8),
+                                  _array(scales_out, "scales_out", (N,), torch.float32), N, K, _raw_stream(stream))
+    _check(st, "vq_quant_rows_int8")
+    return q_out, scales_out
+
+
+def rotate(q, k, inv_freq, ctx_len, *, tree_mask=None, interleaved: bool = False, scale: float = 1.0, q_out=None,
+           k_out=None, stream=None):
+    """Queries and keys turned by their positions (rotary positions).
+
+    q: float16 / bfloat16 [B][n][Hq][D]; k: [B][n][H][D] of the same type, or
+    None (both may be slices of one fused projection); inv_freq: float32
+    [rot / 2], the frequencies of the first rot channels' pairs: (i, i + rot /
+    2), or (2 i, 2 i + 1) where interleaved; ctx_len: int32 [B].  Row i is at
+    position ctx_len[b] + i, or with tree_mask (int64 [B][n], as for
+    tree_attention) ctx_len[b] + the number of set bits below i: the node's
+    depth.  scale multiplies the turned channels (the amplitude of some
+    long-context scalings).  Returns (q_out, k_out); given, they may be q and k
+    themselves (in place)."""
+    torch = _torch()
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [batch][n][heads][head_dim]")
+    shape = B, n, Hq, D = tuple(q.shape)
+    dtype = q.dtype
+    if k is not None and k.dtype != dtype:
+        raise TypeError("q and k must have one dtype")
+    H = 0 if k is None else k.shape[2]
+    kv_shape = (B, n, H, D)
+    qs, ks = _rows(q, "q", shape), 0 if k is None else _rows(k, "k", kv_shape)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    if k is None and k_out is not None:
+        raise ValueError("k_out goes with k")
+    _here(q, k, inv_freq, ctx_len, tree_mask, q_out, k_out)
+    qos, kos = Hq * D, H * D
+    if q_out is not None:
+        qos = _turned_rows(q_out, "q_out", q, shape)
+    if k_out is not None:
+        kos = _turned_rows(k_out, "k_out", k, kv_shape)
+    if q_out is not None or k_out is not None:
+        ins = {"q": (q, qs, Hq * D)} if k is None else {"q": (q, qs, Hq * D), "k": (k, ks, H * D)}
+        for name, out, so, width in (("q_out", q_out, qos, Hq * D), ("k_out", k_out, kos, H * D)):
+            if out is None:
+                continue
+            _apart(out, name, inv_freq=inv_freq, ctx_len=ctx_len, tree_mask=tree_mask)
+            for other, (t, stride, w) in ins.items():
+                in_place = other == name[0] and out.data_ptr() == t.data_ptr() and so == stride
+                if not in_place and _share_rows(out, so, width, t, stride, w):
+                    raise ValueError("%s must not share memory with %s (in place, the rows must be those of the input)"
+                                     % (name, other))
+        if q_out is not None and k_out is not None and _share_rows(q_out, qos, Hq * D, k_out, kos, H * D):
+            raise ValueError("q_out must not share memory with k_out")
+    if q_out is None:
+        q_out = _like(q, stream)
+    if k is not None and k_out is None:
+        k_out = _like(k, stream)
+    st = lib().vq_rotate(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, _dtype_code(q),
+                         _array(inv_freq, "inv_freq", (inv_freq.shape[0],), torch.float32),
+                         _array(ctx_len, "ctx_len", (B,), torch.int32),
+                         _array(tree_mask, "tree_mask", (B, n), torch.int64), q_out.data_ptr(), qos,
+                         None if k is None else k_out.data_ptr(), kos, B, n, Hq, H, D, 2 * inv_freq.shape[0],
+                         int(interleaved), scale, _raw_stream(stream))
+    _check(st, "vq_rotate")
+    return q_out, k_out
+
+
+def _turned_rows(out, name, t, shape):
+    """Row stride of a given output of rotate."""
+    if out.dtype != t.dtype:
+        raise TypeError("%s must have the dtype of its input" % name)
+    return _rows(out, name, shape)
+
+
+def _share_rows(a, a_stride, a_width, b, b_stride, b_width):
+    """Whether two tensors of evenly spaced rows share memory: slices of one
+    fused matrix lie between each other without doing so."""
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    if a1 <= b0 or b1 <= a0:
+        return False
+    if a_stride != b_stride:
+        return True
+    at = (b0 - a0) // a.element_size() % a_stride  # where a row of b begins in a row of a
+    return at < a_width or at + b_width > a_stride

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, "libvq.so")
 
 SOURCES = ["verify_gemm.hip", "w4a8_gemm.hip", "fp8_prefill.hip", "h32_quant.hip", "greedy_verify.hip",
            "hbm_probe.hip", "verify_noalloc.hip", "vq_api.cpp", "tree_attention.hip", "tree_verify.hip",
-           "kv_append.hip", "tree_api.cpp"]
+           "kv_append.hip", "tree_api.cpp", "w8a8_gemm.hip", "row_norm.hip", "rotate.hip", "layer_api.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

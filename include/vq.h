@@ -625,6 +625,136 @@ int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_strid
                  int64_t page_size, int64_t n_pages, int64_t max_pages, void *stream);
 
 /*
+ * The rest of a decoder layer -- the operations between the projections and
+ * the attention of a step, for weights that are 8-bit integers with one scale
+ * per output channel (next to Q4_0 and FP8 tiles, the third common form).
+ * One layer of a step: vq_residual_norm (8-bit rows), vq_gemm_w8a8 (queries,
+ * keys, values), vq_rotate, vq_tree_attention, vq_quant_rows_int8,
+ * vq_gemm_w8a8, vq_residual_norm, vq_gated_w8a8, vq_quant_rows_int8,
+ * vq_gemm_w8a8.
+ *
+ * Alignment here: 16 bytes for matrices and rows, 8 bytes for tree_mask, 4
+ * bytes for scales, biases, frequencies and lengths (slices of longer arrays).
+ */
+#define VQ_MAX_W8A8_K 131056       /* the largest multiple of 16 whose dot of any codes stays in 32 bits */
+#define VQ_MAX_ROW 32768           /* longest row of the norm and of the row quantizer */
+#define VQ_MAX_ROTATE_DIM 512      /* largest head of vq_rotate */
+
+/* Activations of vq_gated_w8a8. */
+#define VQ_ACT_SILU 0              /* g / (1 + exp(-g)) */
+#define VQ_ACT_GELU 1              /* g Phi(g), Phi the normal distribution function */
+#define VQ_ACT_GELU_TANH 2         /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+
+/*
+ * vq_gemm_w8a8 -- out[n][m] = x_scales[n] * w_scales[m] * sum_k x[n][k] w[m][k]
+ *                             + bias[m]
+ *   w         int8 [M][K], w_scales fp32 [M]: any codes, -128 included
+ *   x         int8 [N][K], x_scales fp32 [N], as vq_quant_rows_int8 and
+ *             vq_residual_norm write them
+ *   bias      fp32 [M] or NULL
+ *   out       [N][M], out_dtype F16, BF16 or F32
+ * The sum is an exact 32-bit integer; it is converted to fp32, multiplied by
+ * the row's scale, then by the channel's, the bias added, and the result
+ * rounded to out_dtype: each of these one fp32 operation.  Output bits are
+ * therefore the same for any N, any neighbouring rows, with and without a
+ * workspace and on every device.
+ * Sizes: 1 <= N, M <= VQ_MAX_DIM; 16 <= K <= VQ_MAX_W8A8_K, K % 16 == 0.
+ */
+int vq_gemm_w8a8(const int8_t *w, const float *w_scales, const int8_t *x, const float *x_scales, const float *bias,
+                 void *out, int out_dtype, int64_t n_rows, int64_t m, int64_t k,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * vq_gated_w8a8 -- out[n][f] = act(g[n][f]) * u[n][f], where g and u are the
+ * products of vq_gemm_w8a8 (no bias) with w_gate and w_up, [F][K] each: both
+ * projections of a gated feed-forward block, its activation and the product in
+ * one pass over the weights; g and u are not stored.  g, u, act and their
+ * product are fp32, rounded once.  w_gate and w_up may be the halves of one
+ * [2 F][K] matrix.  Same sizes (F in place of M) and reproducibility.
+ * Returns VQ_ERR_BAD_CONFIG for an unknown activation.
+ */
+int vq_gated_w8a8(const int8_t *w_gate, const float *gate_scales, const int8_t *w_up, const float *up_scales,
+                  const int8_t *x, const float *x_scales, int activation, void *out, int out_dtype,
+                  int64_t n_rows, int64_t f, int64_t k, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * vq_residual_norm -- the residual update behind one block and the norm before
+ * the next.  Per row of C channels:
+ *   u = y                       or post_weight[c] y / sqrt(mean(y^2) + eps)
+ *   x = residual + alpha * gate * u          (gate NULL: 1; y NULL: x = residual)
+ *   residual_out = x, rounded to the residual's type (NULL: not written)
+ *   h = x / sqrt(mean(x^2) + eps) * weight   (weight NULL: 1)
+ *   out = h rounded to out_dtype F16 or BF16, or for I8 the codes and scale of
+ *         vq_quant_rows_int8 for the row h
+ * All of it fp32, from x before its rounding; a row's sum of squares must stay
+ * below the fp32 maximum.
+ *   residual  [N][C], residual_dtype F16, BF16 or F32; residual_out may be
+ *             residual (in place)
+ *   y         [N][C], y_dtype F16 or BF16, or NULL (then post_weight, gate and
+ *             residual_out must be NULL: VQ_ERR_BAD_CONFIG)
+ *   post_weight, weight  fp32 [C] or NULL
+ *   gate      fp32 [C], or with gate_rows != 0 [N][C] of y's type; or NULL
+ *   eps       >= 0 and finite (VQ_ERR_BAD_CONFIG)
+ *   scales_out  fp32 [N] for I8, NULL otherwise
+ * A row's outputs depend on that row alone.
+ * Sizes: 1 <= N <= VQ_MAX_DIM, 16 <= C <= VQ_MAX_ROW, C % 16 == 0.
+ */
+int vq_residual_norm(const void *residual, int residual_dtype, const void *y, int y_dtype,
+                     const float *post_weight, const void *gate, int gate_rows, float alpha,
+                     const float *weight, float eps, void *residual_out, void *out, int out_dtype,
+                     float *scales_out, int64_t n_rows, int64_t c, void *stream);
+
+/*
+ * vq_quant_rows_int8 -- 8-bit codes of rows, one scale per row:
+ *   s = max_k |x[n][k]| / 127                        -> scales_out fp32 [N]
+ *   q = clamp(rint_half_even(x[n][k] / s), -127, 127) -> q_out int8 [N][K]
+ * Both divisions are IEEE fp32, correctly rounded, so codes and scales are
+ * reproducible bit for bit.  A row of zeros (or one whose s is below the
+ * smallest fp32 number) gets codes 0.  A row that holds a NaN or an infinity
+ * gets the scale NaN and codes 0, so that it shows in the products.
+ * x_dtype F16, BF16 or F32.  Sizes: 1 <= N <= VQ_MAX_DIM,
+ * 16 <= K <= VQ_MAX_ROW, K % 16 == 0.
+ */
+int vq_quant_rows_int8(const void *x, int x_dtype, int8_t *q_out, float *scales_out,
+                       int64_t n_rows, int64_t k, void *stream);
+
+/*
+ * vq_rotate -- queries and keys turned by their positions (rotary positions),
+ * for the nodes of drafted trees or for prompts.  Row i of sequence b is at
+ *   p = ctx_len[b] + (number of j < i with bit j of tree_mask[b][i] set)
+ * (tree_mask NULL: a chain, p = ctx_len[b] + i; ctx_len taken as 0 where
+ * negative): with the masks of vq_tree_attention whose bits are a node and
+ * its ancestors, a node's depth.  Pair i < rot_dim / 2 of each head, elements
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) where interleaved != 0, becomes
+ *   (a, b) -> scale * (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i]
+ * and elements from rot_dim on are copied.  t is formed and reduced in 64
+ * bits; sin, cos and the rest are fp32, rounded once to dtype.  inv_freq holds
+ * whatever the model's scaling for long contexts makes of its frequencies, and
+ * `scale` its amplitude (1 without).
+ *   q, k      [batch * n] rows of q_heads (kv_heads) * head_dim elements,
+ *             q_stride (k_stride) elements apart: slices of a fused projection;
+ *             k may be NULL with k_out (queries alone)
+ *   q_out, k_out  rows likewise; each may be its input (in place, same stride)
+ *   inv_freq  fp32 [rot_dim / 2], finite
+ *   tree_mask uint64 [batch][n] or NULL
+ * Sizes: head_dim and rot_dim multiples of 16, 16 <= rot_dim <= head_dim <=
+ * VQ_MAX_ROTATE_DIM; n <= VQ_MAX_TREE_NODES with tree_mask; batch * n <=
+ * VQ_MAX_DIM / 2; heads and strides as for vq_tree_attention.
+ */
+int vq_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int dtype,
+              const float *inv_freq, const int32_t *ctx_len, const uint64_t *tree_mask,
+              void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+              int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
+              int interleaved, float scale, void *stream);
+
+/* Workspace bytes of the two products for any number of rows (0 for sizes
+ * outside the limits, or where none is used).  As for the verify GEMMs:
+ * zero-filled once by the caller, left ready for the next call, not shared by
+ * calls that overlap in time; NULL or a smaller one runs a slower form. */
+size_t vq_w8a8_workspace_bytes(int64_t m, int64_t k);
+size_t vq_gated_w8a8_workspace_bytes(int64_t f, int64_t k);
+
+/*
  * vq_hbm_read_probe -- a plain read of `bytes` of device memory at `buf`,
  * the bandwidth the verify GEMM's weight stream is measured against ([P1]
  * TL;DR: decode streams the weights at a fraction of the card's bandwidth,
