@@ -92,8 +92,7 @@ SIGNATURES = {
                           _I64, _I64, _P]),
     "vq_gemm_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
     "vq_gated_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
-    "vq_w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
-    "vq_gated_w8a8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "vq_w8a8_workspace_bytes": (_SZ, [_I64]),
     "vq_residual_norm": (_I, [_P, _I, _P, _I, _P, _P, _I, _F, _P, _F, _P, _P, _I, _P, _I64, _I64, _P]),
     "vq_quant_rows_int8": (_I, [_P, _I, _P, _P, _I64, _I64, _P]),
     "vq_rotate": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I,
@@ -992,7 +991,7 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     _here(w, w_scales, x, x_scales, bias, out)
     _apart(out, "out", w=w, w_scales=w_scales, x=x, x_scales=x_scales, bias=bias)
     sh = _raw_stream(stream)
-    wp, wn = _w8a8_workspace("vq_w8a8_workspace_bytes", M, K, workspace, x.device, sh)
+    wp, wn = _w8a8_workspace(N, workspace, x.device, sh)
     st = lib().vq_gemm_w8a8(_array(w, "w", (M, K), i8), _array(w_scales, "w_scales", (M,), f32),
                             _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
                             _array(bias, "bias", (M,), f32), _dev_ptr(out, "out"), _dtype_code(out), N, M, K, wp, wn,
@@ -1001,11 +1000,11 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     return out
 
 
-def _w8a8_workspace(query, m, k, workspace, device, stream_handle):
-    """(pointer, bytes) for a product of 8-bit codes."""
+def _w8a8_workspace(n, workspace, device, stream_handle):
+    """(pointer, bytes) for a product of 8-bit codes with n rows."""
     if workspace is None:
         return None, 0
-    ws = _sized_workspace(query, (m, k), workspace, device, stream_handle)
+    ws = _sized_workspace("vq_w8a8_workspace_bytes", (n,), workspace, device, stream_handle)
     return ws.ptr(), ws.nbytes
 
 
@@ -1030,7 +1029,7 @@ def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activa
     _apart(out, "out", w_gate=w_gate, gate_scales=gate_scales, w_up=w_up, up_scales=up_scales, x=x,
            x_scales=x_scales)
     sh = _raw_stream(stream)
-    wp, wn = _w8a8_workspace("vq_gated_w8a8_workspace_bytes", F, K, workspace, x.device, sh)
+    wp, wn = _w8a8_workspace(N, workspace, x.device, sh)
     st = lib().vq_gated_w8a8(_array(w_gate, "w_gate", (F, K), i8), _array(gate_scales, "gate_scales", (F,), f32),
                              _array(w_up, "w_up", (F, K), i8), _array(up_scales, "up_scales", (F,), f32),
                              _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
@@ -1039,14 +1038,9 @@ def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activa
     return out
 
 
-def w8a8_workspace_bytes(m: int, k: int) -> int:
-    """Workspace bytes of gemm_w8a8 for any number of rows."""
-    return int(lib().vq_w8a8_workspace_bytes(m, k))
-
-
-def gated_w8a8_workspace_bytes(f: int, k: int) -> int:
-    """Workspace bytes of gated_w8a8 for any number of rows."""
-    return int(lib().vq_gated_w8a8_workspace_bytes(f, k))
+def w8a8_workspace_bytes(n_rows: int) -> int:
+    """Workspace bytes of gemm_w8a8 and gated_w8a8 for n_rows rows."""
+    return int(lib().vq_w8a8_workspace_bytes(n_rows))
 
 
 def residual_norm(residual, y=None, weight=None, *, out, scales_out=None, residual_out=None, post_weight=None,

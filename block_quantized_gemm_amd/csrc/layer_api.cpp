@@ -63,11 +63,8 @@ int run_product(const vq::W8A8Args &a, int64_t n, int64_t m, int64_t k) {
 
 extern "C" {
 
-size_t vq_w8a8_workspace_bytes(int64_t m, int64_t k) {
-    return product_ok(m, k) ? vq::w8a8_workspace(false, (int)m, (int)k) : 0;
-}
-size_t vq_gated_w8a8_workspace_bytes(int64_t f, int64_t k) {
-    return product_ok(f, k) ? vq::w8a8_workspace(true, (int)f, (int)k) : 0;
+size_t vq_w8a8_workspace_bytes(int64_t n_rows) {
+    return in(n_rows, 1, VQ_MAX_DIM) ? vq::w8a8_workspace((int)n_rows) : 0;
 }
 
 int vq_gemm_w8a8(const int8_t *w, const float *w_scales, const int8_t *x, const float *x_scales, const float *bias,

@@ -29,7 +29,7 @@ struct W8A8Args {
     hipStream_t stream;
 };
 hipError_t launch_w8a8(const W8A8Args &a);
-size_t w8a8_workspace(bool gated, int M, int K);
+size_t w8a8_workspace(int N);  // for N rows of any product
 
 // Arguments of one residual update with its norms, or of a row quantization
 // (residual alone, no weight, raw: the rows as they are), already checked.

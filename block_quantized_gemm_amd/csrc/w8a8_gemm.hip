@@ -15,6 +15,8 @@
 // 128 k are loaded straight into LDS, `STAGES - 1` chunks ahead; 16-byte pieces
 // are XOR-swizzled by row so that the operand reads of 16 rows cover all 64
 // banks.
+#include <atomic>
+
 #include "layer_internal.h"
 #include "vq_device.h"
 
@@ -22,14 +24,21 @@ namespace vq {
 
 namespace {
 
-constexpr int kChunk = 128;            // k per chunk: one 128-byte line of a row
 constexpr int kOutOfRange = 0x7FFFFFF0;  // past every range below: the load returns zeros
+constexpr int kCoherent = 0x10;          // sc1: agent-coherent, no cache maintenance needed
+constexpr int kMaxGroups = 512;          // persistent workgroups of a launch
+constexpr size_t kCounterBytes = kMaxGroups * 8 * 4;  // a tile cut between workgroups: one counter per wave
+constexpr int kStrip = 4;                // feature columns of tiles walked together
 
 struct KArgs {
     const int8_t *w, *up, *x;
     const float *w_scales, *up_scales, *x_scales, *bias;
     void *out;
-    int N, M, K, out_dtype, activation, row_tiles;
+    uint32_t *counters;  // and the pieces behind them
+    int N, M, K, out_dtype, activation;
+    int row_tiles, col_tiles;
+    int whole;   // tiles that every workgroup computes alone, in turn
+    int ranges;  // workgroups that share the chunks of the tiles after those
 };
 
 __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
@@ -50,165 +59,405 @@ __device__ __forceinline__ float activate(float g, int kind) {
     return 0.5f * g * erfcf(g * -0.7071067811865476f);
 }
 
-template <int RT, int FT, int WR, int WF, int STAGES, bool GATED>
+// A piece of work: chunks [c0, c1) of one tile.
+struct Part {
+    int tile, c0, c1;
+};
+
+// RT x FT tiles of 16 rows x 16 features per wave, WR x WF waves, chunks of KC
+// k in STAGES stages.
+template <int RT, int FT, int WR, int WF, int KC, int STAGES, bool GATED>
 __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
     constexpr int kWaves = WR * WF, BM = 16 * RT * WR, BF = 16 * FT * WF;
-    constexpr int kWPieces = BF / 8, kPieces = kWPieces + BM / 8;  // 1 KiB each: 8 rows x 128 B
+    constexpr int kSlots = KC / 16, kPieceRows = 64 / kSlots;  // a wave loads pieces of 1 KiB: so many rows of KC bytes
+    constexpr int kWPieces = BF / kPieceRows, kXPieces = BM / kPieceRows, kPieces = kWPieces + kXPieces;
     constexpr int kPer = kPieces / kWaves, kExtra = kPieces % kWaves, kMost = kPer + (kExtra ? 1 : 0);
     constexpr int kStage = kPieces * 1024;
     constexpr int kOutFeats = GATED ? BF / 2 : BF;  // output features of the workgroup
     constexpr int FO = GATED ? FT / 2 : FT;         // output feature tiles of a wave
-    static_assert(kWaves % 2 == 0 && (!GATED || FT % 2 == 0), "shape");
+    constexpr int kSlot = BM * BF * 4;              // bytes of a tile's sums
+    constexpr int kSteps = KC / 64;                 // MFMA steps of a chunk
+    static_assert(KC == 64 || KC == 128, "chunk");
+    static_assert(kWaves <= 8 && (KC == 64 || kWaves % 2 == 0) && (!GATED || FT % 2 == 0), "shape");
+    static_assert(kWPieces % (GATED ? 2 * kWaves : kWaves) == 0, "a wave's i-th piece is of the same matrix in every wave");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = wave_id(), j = lane & 15, g = lane >> 4;
     const int wr = wave % WR, wf = wave / WR;
-    const int tile = xcd_run_index((int)blockIdx.x, (int)gridDim.x);
-    const int fb = tile / a.row_tiles * kOutFeats, rb = tile % a.row_tiles * BM;
-    const int K = a.K, nch = (K + kChunk - 1) / kChunk;
+    const int G = (int)gridDim.x, me = xcd_run_index((int)blockIdx.x, G);
+    const int K = a.K, nch = (K + KC - 1) / KC;
+    const int alone = a.whole / G + (me < a.whole % G ? 1 : 0);
+    // the chunks after the whole tiles, in even ranges: mine are [u0, u1)
+    const int R = (a.row_tiles * a.col_tiles - a.whole) * nch;
+    const int u0 = me < a.ranges ? (int)((int64_t)me * R / a.ranges) : 0;
+    const int u1 = me < a.ranges ? (int)((int64_t)(me + 1) * R / a.ranges) : 0;
+    const int first = u0 / nch;
+    const int parts = alone + (u1 > u0 ? (u1 - 1) / nch - first + 1 : 0);
+    if (parts == 0)
+        return;
+    const auto part = [&](int i) -> Part {
+        if (i < alone)
+            return Part{i * G + me, 0, nch};
+        const int t = first + i - alone;
+        return Part{a.whole + t, max(u0 - t * nch, 0), min(u1 - t * nch, nch)};
+    };
+    // tiles in strips of kStrip feature columns, rows of a strip one after the
+    // other: neighbours, which run on one XCD, share rows and columns in its L2
+    const auto place = [&](int tile, int &fb, int &rb) {
+        const int per = kStrip * a.row_tiles, strip = tile / per, in = tile - strip * per;
+        const int width = min(kStrip, a.col_tiles - strip * kStrip);
+        rb = in / width * BM;
+        fb = (strip * kStrip + in % width) * kOutFeats;
+    };
 
-    const int rows = min(BM, a.N - rb), feats = min(kOutFeats, a.M - fb);
-    const rsrc_t rx = make_rsrc(a.x + (size_t)rb * K, (uint32_t)rows * (uint32_t)K);
-    const rsrc_t rw = make_rsrc(a.w + (size_t)fb * K, (uint32_t)feats * (uint32_t)K);
-    const rsrc_t ru = GATED ? make_rsrc(a.up + (size_t)fb * K, (uint32_t)feats * (uint32_t)K) : rw;
-    // row 8 p + lane / 8 of a piece p = wave + kWaves i, its 16-byte slot lane % 8:
-    // the slot holds the row's bytes 16 (slot ^ (row / 2 % 8)) .. +16
-    const int byte16 = 16 * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
-    const int voff = (lane >> 3) * K + byte16;
-
-    auto issue = [&](int c, int stage) {
-        const int k0 = c * kChunk;
+    // Piece p = wave + kWaves i of a chunk holds rows kPieceRows p .. of it; a
+    // row's 16-byte slot s holds its bytes 16 (s ^ swizzle(row)) .. +16, where
+    // the swizzle counts rows of 256 bytes (all 64 banks)
+    const int prow = lane / kSlots;
+    const int swz = KC == 128 ? 4 * (wave & 1) + (lane >> 4) : lane >> 4;
+    const int byte16 = 16 * ((lane & (kSlots - 1)) ^ swz);
+    const int voff = prow * K + byte16;
+    rsrc_t rx, rw, ru;
+    int at = -1, lc = 0, lend = 0;  // the part whose chunks are being loaded
+    const auto open = [&]() {
+        if (++at >= parts) {
+            lc = -1;  // nothing left: what follows loads zeros
+            return;
+        }
+        const Part p = part(at);
+        int fb, rb;
+        place(p.tile, fb, rb);
+        lc = p.c0;
+        lend = p.c1;
+        const uint32_t feats = (uint32_t)min(kOutFeats, a.M - fb);
+        rx = make_rsrc(a.x + (size_t)rb * K, (uint32_t)min(BM, a.N - rb) * (uint32_t)K);
+        rw = make_rsrc(a.w + (size_t)fb * K, feats * (uint32_t)K);
+        if constexpr (GATED)
+            ru = make_rsrc(a.up + (size_t)fb * K, feats * (uint32_t)K);
+    };
+    const auto issue = [&](int stage) {
+        const int k0 = max(lc, 0) * KC;
         // past K the row's neighbour would be read: the activations are
         // zeros there, and so is the product
-        const int xoff = k0 + byte16 < K ? voff : kOutOfRange;
-        const int woff = c < nch ? voff : kOutOfRange;
-        uint8_t *st = lds + stage * kStage;
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int p = wave + kWaves * i;
-            if (kExtra && i == kMost - 1 && p >= kPieces)
-                break;
-            if (p >= kWPieces)
-                bload16_lds(rx, st + 1024 * p, xoff, 8 * (p - kWPieces) * K + k0);
-            else if (GATED && p >= kWPieces / 2)
-                bload16_lds(ru, st + 1024 * p, woff, 8 * (p - kWPieces / 2) * K + k0);
-            else
-                bload16_lds(rw, st + 1024 * p, woff, 8 * p * K + k0);
-        }
+        const int woff = lc < 0 ? kOutOfRange : voff;
+        const int xoff = k0 + byte16 < K ? woff : kOutOfRange;
+        uint8_t *st = lds + stage * kStage + wave * 1024;
+        const int step = kWaves * kPieceRows * K;  // a wave's next piece
+        const int base = wave * kPieceRows * K + k0;
+        static_for<kMost>([&](auto I) {
+            constexpr int i = I.value, x0 = kWPieces / kWaves, up0 = x0 / 2;
+            if constexpr (i >= x0) {
+                if (kExtra == 0 || i < kMost - 1 || wave < kExtra)
+                    bload16_lds(rx, st + 1024 * kWaves * i, xoff, base + (i - x0) * step);
+            } else if constexpr (GATED && i >= up0) {
+                bload16_lds(ru, st + 1024 * kWaves * i, woff, base + (i - up0) * step);
+            } else {
+                bload16_lds(rw, st + 1024 * kWaves * i, woff, base + i * step);
+            }
+        });
+        if (lc >= 0 && ++lc == lend)
+            open();
     };
 
     i32x4 acc[FT][RT];
-#pragma unroll
-    for (int ft = 0; ft < FT; ++ft)
+    u32x4 xb[kSteps][RT], wa[kSteps][FT];
+    const int sw = KC == 128 ? (j >> 1) & 7 : j >> 2;
+    const uint8_t *xs = lds + kWPieces * 1024 + (wr * RT * 16 + j) * KC;
+    const uint8_t *ws = lds + (wf * FO * 16 + j) * KC;
+    const auto read_x = [&](int s, int rt, int stage) {
+        return *reinterpret_cast<const u32x4 *>(xs + stage * kStage + rt * 16 * KC + 16 * ((4 * s + g) ^ sw));
+    };
+    const auto read_w = [&](int s, int ft, int stage) {
+        return *reinterpret_cast<const u32x4 *>(ws + stage * kStage + (ft < FO ? ft * 16 : BF / 2 + (ft - FO) * 16) * KC +
+                                                16 * ((4 * s + g) ^ sw));
+    };
+    const auto landed = [&](auto C) {  // all but the newest C chunks' loads
+        if (!kExtra || wave >= kExtra)
+            wait_vmcnt<C.value * kPer>();
+        else
+            wait_vmcnt<C.value * kMost>();
+        lds_barrier();
+    };
+
+    // Sums to outputs, in the accumulators' registers.
+    const auto finish = [&](int fb, int rb) {
+        const rsrc_t rg = make_rsrc(a.w_scales, (uint32_t)a.M * 4u);
+        const rsrc_t rs = make_rsrc(a.x_scales + rb, (uint32_t)(a.N - rb) * 4u);
+        float sx[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-            acc[ft][rt] = i32x4{0, 0, 0, 0};
-
+            sx[rt] = __builtin_bit_cast(float, bload4<kAuxCached>(rs, 4 * (wr * RT * 16 + rt * 16 + j), 0));
+        const int f0 = fb + wf * FO * 16 + 4 * g;
+        if constexpr (GATED) {
+            const rsrc_t rsu = make_rsrc(a.up_scales, (uint32_t)a.M * 4u);
+            const auto all = [&](auto KIND) {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        issue(s, s);
-    const int sw = (j >> 1) & 7;
-    int stage = 0;
-    for (int c = 0; c < nch; ++c) {
-        // all but the newest STAGES - 2 chunks' loads have landed
-        if (!kExtra || wave >= kExtra)
-            wait_vmcnt<(STAGES - 2) * kPer>();
-        else
-            wait_vmcnt<(STAGES - 2) * kMost>();
-        lds_barrier();  // chunk c is whole, and every wave is done with chunk c - 1
-        issue(c + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-        const uint8_t *st = lds + stage * kStage;
-        const uint8_t *xs = st + kWPieces * 1024 + (wr * RT * 16 + j) * 128;
-        const uint8_t *wl = st + (wf * FO * 16 + j) * 128;
+                for (int ft = 0; ft < FO; ++ft)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int at = 16 * ((4 * s + g) ^ sw);
-            u32x4 xb[RT], wa[FT];
+                    for (int r = 0; r < 4; ++r) {
+                        const int o = 4 * (f0 + ft * 16 + r);
+                        const float sg = __builtin_bit_cast(float, bload4<kAuxCached>(rg, o, 0));
+                        const float su = __builtin_bit_cast(float, bload4<kAuxCached>(rsu, o, 0));
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const float gate = activate((float)acc[ft][rt][r] * sx[rt] * sg, KIND.value);
+                            acc[ft][rt][r] =
+                                __builtin_bit_cast(int, gate * ((float)acc[ft + FO][rt][r] * sx[rt] * su));
+                        }
+                    }
+            };
+            if (a.activation == VQ_ACT_SILU)
+                all(std::integral_constant<int, VQ_ACT_SILU>{});
+            else if (a.activation == VQ_ACT_GELU)
+                all(std::integral_constant<int, VQ_ACT_GELU>{});
+            else
+                all(std::integral_constant<int, VQ_ACT_GELU_TANH>{});
+        } else {
+            const bool biased = a.bias != nullptr;
+            const rsrc_t rb4 = make_rsrc(biased ? a.bias : a.w_scales, (uint32_t)a.M * 4u);
 #pragma unroll
             for (int ft = 0; ft < FT; ++ft)
-                wa[ft] = *reinterpret_cast<const u32x4 *>(
-                    wl + (ft < FO ? ft * 16 : BF / 2 + (ft - FO) * 16) * 128 + at);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int o = 4 * (f0 + ft * 16 + r);
+                    const float sg = __builtin_bit_cast(float, bload4<kAuxCached>(rg, o, 0));
+                    // (-0 + y is y: no bias changes no bit)
+                    const float add = biased ? __builtin_bit_cast(float, bload4<kAuxCached>(rb4, o, 0)) : -0.0f;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        acc[ft][rt][r] = __builtin_bit_cast(int, (float)acc[ft][rt][r] * sx[rt] * sg + add);
+                }
+        }
+    };
+    const auto store = [&](int fb, int rb) {
+        const int f0 = fb + wf * FO * 16 + 4 * g, n0 = rb + wr * RT * 16 + j;
+        const auto all = [&](auto OD, auto VEC) {
+            constexpr int esz = OD.value == VQ_DTYPE_F32 ? 4 : 2;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int n = n0 + rt * 16;
+                uint8_t *row = static_cast<uint8_t *>(a.out) + ((size_t)n * (size_t)a.M + (size_t)f0) * esz;
+                if (n < a.N) {
+#pragma unroll
+                    for (int ft = 0; ft < FO; ++ft) {
+                        float v[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int bits = acc[ft][rt][r];  // (a cast of the element itself reads element 0)
+                            v[r] = __builtin_bit_cast(float, bits);
+                        }
+                        if constexpr (VEC.value) {
+                            if (f0 + ft * 16 < a.M) {
+                                if constexpr (OD.value == VQ_DTYPE_F32) {
+                                    *reinterpret_cast<f32x4 *>(row + ft * 64) = f32x4{v[0], v[1], v[2], v[3]};
+                                } else {
+                                    uint16_t h[4];
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r)
+                                        if constexpr (OD.value == VQ_DTYPE_BF16)
+                                            h[r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[r]));
+                                        else
+                                            h[r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[r]));
+                                    *reinterpret_cast<u32x2 *>(row + ft * 32) =
+                                        u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (f0 + ft * 16 + r < a.M)
+                                    store_out(row, OD.value, ft * 16 + r, v[r]);
+                        }
+                    }
+                }
+            }
+        };
+        const auto typed = [&](auto VEC) {
+            if (a.out_dtype == VQ_DTYPE_F32)
+                all(std::integral_constant<int, VQ_DTYPE_F32>{}, VEC);
+            else if (a.out_dtype == VQ_DTYPE_BF16)
+                all(std::integral_constant<int, VQ_DTYPE_BF16>{}, VEC);
+            else
+                all(std::integral_constant<int, VQ_DTYPE_F16>{}, VEC);
+        };
+        if (a.M % 4 == 0)  // 4 features of a row are aligned
+            typed(std::true_type{});
+        else
+            typed(std::false_type{});
+    };
+
+    // A tile cut between workgroups: each stores its sums, agent-coherent and
+    // waited for, then counts in; the last adds the others' to its own.  Per
+    // wave: the waves of a tile's workgroups hold the same outputs.
+    const auto join = [&](const Part &p) -> bool {
+        const rsrc_t rp = make_rsrc(reinterpret_cast<uint8_t *>(a.counters) + kCounterBytes,
+                                    (uint32_t)a.ranges * 2u * (uint32_t)kSlot);
+        const int t = p.tile - a.whole;
+        const int b0 = (int)(((int64_t)(t * nch + 1) * a.ranges - 1) / R);
+        const int b1 = (int)(((int64_t)(t + 1) * nch * a.ranges - 1) / R);
+        const auto slot = [&](int who) {
+            const int begins = (int)((int64_t)who * R / a.ranges) / nch;  // the first tile of its range
+            return (2 * who + (begins == t ? 0 : 1)) * kSlot + wave * FT * RT * 1024;
+        };
+        const int mine = slot(me);
+#pragma unroll
+        for (int ft = 0; ft < FT; ++ft)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                xb[rt] = *reinterpret_cast<const u32x4 *>(xs + rt * 16 * 128 + at);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[ft][rt]), rp,
+                                                       16 * lane + (ft * RT + rt) * 1024, mine, kCoherent);
+        wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
+        uint32_t *count = a.counters + t * kWaves + wave;
+        uint32_t old = 0;
+        if (lane == 0)
+            old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (__builtin_amdgcn_readfirstlane(old) != (uint32_t)(b1 - b0))
+            return false;
+        if (lane == 0)  // every piece has arrived: the counter is ready for the next call
+            __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("" ::: "memory");
+        // so many loads go out together, of kBatch workgroups' pieces or of a part of one
+        constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 8 ? kTiles : 8, kBatch = 8 / kAtOnce;
+        for (int w0 = b0; w0 <= b1; w0 += kBatch) {
+            static_for<kTiles / kAtOnce>([&](auto H) {
+                u32x4 v[kBatch][kAtOnce];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const int who = w0 + q;
+                    const bool other = who <= b1 && who != me;
+                    const int theirs = other ? slot(who) : 0;
+                    const int off = other ? 16 * lane : kOutOfRange;
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e)
+                        v[q][e] = __builtin_amdgcn_raw_buffer_load_b128(rp, off + (H.value * kAtOnce + e) * 1024,
+                                                                        theirs, kCoherent);
+                }
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e) {
+                        constexpr int t0 = H.value * kAtOnce;
+                        acc[(t0 + e) / RT][(t0 + e) % RT] += __builtin_bit_cast(i32x4, v[q][e]);
+                    }
+            });
+        }
+        return true;
+    };
+
+    // The operands of a chunk are read while the one before it is multiplied:
+    // its stage is free from the next barrier on, and takes the chunk STAGES
+    // ahead.
+    open();
+#pragma unroll 1
+    for (int s = 0; s < STAGES; ++s)
+        issue(s);
+    landed(std::integral_constant<int, STAGES - 1>{});
+    int stage = 0;
+    for (int i = 0; i < parts; ++i) {
+        const Part p = part(i);
+#pragma unroll
+        for (int ft = 0; ft < FT; ++ft)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
+                acc[ft][rt] = i32x4{0, 0, 0, 0};
+        // a part's first operands (again: nothing is held over the end of a part)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+            for (int ft = 0; ft < FT; ++ft)
+                wa[s][ft] = read_w(s, ft, stage);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                xb[s][rt] = read_x(s, rt, stage);
+        }
+        for (int c = p.c0; c < p.c1; ++c) {
+            landed(std::integral_constant<int, STAGES - 2>{});
+            issue(stage);
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            u32x4 wn[kSteps][FT];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int ft = 0; ft < FT; ++ft)
-                    acc[ft][rt] = mfma_i8(wa[ft], xb[rt], acc[ft][rt]);
-        }
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-    wait_vmcnt<0>();  // the loads past the last chunk write LDS: none outlives the workgroup
-
-    const size_t M = (size_t)a.M;
-    const bool vec = a.M % 4 == 0;
+                    wn[s][ft] = read_w(s, ft, stage);
 #pragma unroll
-    for (int ft = 0; ft < FO; ++ft) {
-        const int f = fb + wf * FO * 16 + ft * 16 + 4 * g;
-        float sg[4], su[4], add[4];
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool in = f + r < a.M;
-            sg[r] = in ? a.w_scales[f + r] : 0.f;
-            su[r] = GATED && in ? a.up_scales[f + r] : 0.f;
-            add[r] = !GATED && a.bias && in ? a.bias[f + r] : 0.f;
-        }
+                for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int n = rb + wr * RT * 16 + rt * 16 + j;
-            if (n >= a.N)
-                continue;
-            const float sx = a.x_scales[n];
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float y = (float)acc[ft][rt][r] * sx * sg[r];
-                if constexpr (GATED)
-                    v[r] = activate(y, a.activation) * ((float)acc[ft + FO][rt][r] * sx * su[r]);
-                else
-                    v[r] = a.bias ? y + add[r] : y;
-            }
-            const size_t at = (size_t)n * M + (size_t)f;
-            if (vec && f < a.M) {
-                if (a.out_dtype == VQ_DTYPE_F32)
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
-                else {
-                    uint16_t h[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        h[r] = a.out_dtype == VQ_DTYPE_BF16
-                                   ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[r]))
-                                   : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[r]));
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at) =
-                        u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+                    for (int ft = 0; ft < FT; ++ft)
+                        acc[ft][rt] = mfma_i8(wa[s][ft], xb[s][rt], acc[ft][rt]);
+                    xb[s][rt] = read_x(s, rt, stage);
                 }
-            } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (f + r < a.M)
-                        store_out(a.out, a.out_dtype, at + r, v[r]);
-            }
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int ft = 0; ft < FT; ++ft)
+                    wa[s][ft] = wn[s][ft];
+        }
+        if (p.c1 - p.c0 == nch || join(p)) {
+            int fb, rb;
+            place(p.tile, fb, rb);
+            finish(fb, rb);
+            store(fb, rb);
         }
     }
+    wait_vmcnt<0>();  // loads past the last chunk write LDS: none outlives the workgroup
 }
 
-template <int RT, int FT, int WR, int WF, int STAGES, bool GATED>
+// How a launch cuts its tiles: `whole` of them by single workgroups, the rest
+// in `ranges` even ranges of chunks.  Without a workspace every tile is whole.
+struct Cut {
+    int groups, whole, ranges;
+};
+
+int device_cus() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64)
+        return 256;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+            n = 256;
+        n = std::min(n, kMaxGroups);
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+Cut cut_of(int64_t tiles, int nch, int most, bool pieces) {
+    const int G = device_cus();
+    const int64_t rem = tiles % G;
+    if (!pieces || rem == 0)
+        return Cut{(int)std::min<int64_t>(tiles, G), (int)tiles, 0};
+    // a tile is cut into `most` pieces at most
+    const int ranges = (int)std::min<int64_t>({(int64_t)G, rem * nch, rem * most});
+    const int whole = (int)(tiles - rem);
+    return Cut{whole ? G : ranges, whole, ranges};
+}
+
+template <int RT, int FT, int WR, int WF, int KC, int STAGES, bool GATED>
 hipError_t launch_shape(const W8A8Args &p) {
     constexpr int BM = 16 * RT * WR, BF = 16 * FT * WF, kOutFeats = GATED ? BF / 2 : BF;
-    constexpr int kLds = STAGES * (BF + BM) * 128;
-    const auto kern = w8a8_kernel<RT, FT, WR, WF, STAGES, GATED>;
+    constexpr int kLds = STAGES * (BF + BM) * KC;
+    const auto kern = w8a8_kernel<RT, FT, WR, WF, KC, STAGES, GATED>;
     const hipError_t e =
         hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess)
         return e;
     const int cols = (p.M + kOutFeats - 1) / kOutFeats, row_tiles = (p.N + BM - 1) / BM;
-    const int per_launch = std::max(1, (1 << 22) / cols);  // row tiles per launch: a grid holds 2^32 - 1 threads
+    const int nch = (p.K + KC - 1) / KC;
+    const int per_launch = std::max(1, (1 << 30) / cols);  // row tiles per launch: tile numbers stay in 32 bits
+    const bool pieces = p.workspace && p.workspace_bytes >= kCounterBytes + (size_t)device_cus() * 2 * BM * BF * 4;
     for (int r0 = 0; r0 < row_tiles; r0 += per_launch) {
         const int rt = std::min(per_launch, row_tiles - r0);
+        const Cut cut = cut_of((int64_t)rt * cols, nch, 8, pieces);
         KArgs a{p.w, p.up, p.x + (size_t)r0 * BM * p.K, p.w_scales, p.up_scales, p.x_scales + (size_t)r0 * BM, p.bias,
                 static_cast<char *>(p.out) + (size_t)r0 * BM * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2),
-                std::min(p.N - r0 * BM, rt * BM), p.M, p.K, p.out_dtype, p.activation, rt};
-        hipLaunchKernelGGL(kern, dim3(cols * rt), dim3(64 * WR * WF), kLds, p.stream, a);
+                static_cast<uint32_t *>(p.workspace), std::min(p.N - r0 * BM, rt * BM), p.M, p.K, p.out_dtype,
+                p.activation, rt, cols, cut.whole, cut.ranges};
+        hipLaunchKernelGGL(kern, dim3(cut.groups), dim3(64 * WR * WF), kLds, p.stream, a);
     }
     return hipGetLastError();
 }
@@ -216,18 +465,21 @@ hipError_t launch_shape(const W8A8Args &p) {
 template <bool GATED>
 hipError_t launch_rows(const W8A8Args &p) {
     if (p.N <= 16)
-        return launch_shape<1, 2, 1, 4, 6, GATED>(p);
+        return launch_shape<1, 2, 1, 4, 128, 6, GATED>(p);
     if (p.N <= 64)
-        return launch_shape<4, 2, 1, 4, 4, GATED>(p);
-    return launch_shape<8, 4, 2, 4, 2, GATED>(p);
+        return launch_shape<4, 2, 1, 4, 128, 4, GATED>(p);
+    if (p.N <= 128)
+        return launch_shape<4, 4, 2, 4, 64, 4, GATED>(p);
+    return launch_shape<8, 4, 2, 4, 64, 4, GATED>(p);
+}
+
+size_t slot_bytes(int n) {
+    return n <= 16 ? 16 * 128 * 4 : n <= 64 ? 64 * 128 * 4 : n <= 128 ? 128 * 256 * 4 : 256 * 256 * 4;
 }
 
 }  // namespace
 
-size_t w8a8_workspace(bool gated, int M, int K) {
-    (void)gated, (void)M, (void)K;
-    return 0;
-}
+size_t w8a8_workspace(int N) { return kCounterBytes + (size_t)device_cus() * 2 * slot_bytes(N); }
 
 hipError_t launch_w8a8(const W8A8Args &p) { return p.up ? launch_rows<true>(p) : launch_rows<false>(p); }
 

@@ -747,12 +747,12 @@ int vq_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, 
               int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t rot_dim,
               int interleaved, float scale, void *stream);
 
-/* Workspace bytes of the two products for any number of rows (0 for sizes
- * outside the limits, or where none is used).  As for the verify GEMMs:
- * zero-filled once by the caller, left ready for the next call, not shared by
- * calls that overlap in time; NULL or a smaller one runs a slower form. */
-size_t vq_w8a8_workspace_bytes(int64_t m, int64_t k);
-size_t vq_gated_w8a8_workspace_bytes(int64_t f, int64_t k);
+/* Workspace bytes of the two products for n_rows rows, whatever M and K (0
+ * for n_rows outside the limits; on an MI355X 4 MiB for a draft block of 16
+ * rows, 128 MiB for prompts).  As for the verify GEMMs: zero-filled once by the
+ * caller, left ready for the next call, not shared by calls that overlap in
+ * time; NULL or a smaller one runs a slower form. */
+size_t vq_w8a8_workspace_bytes(int64_t n_rows);
 
 /*
  * vq_hbm_read_probe -- a plain read of `bytes` of device memory at `buf`,

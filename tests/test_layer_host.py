@@ -50,9 +50,10 @@ def test_gated_activation():
 
 
 def test_product_workspace_sizes():
-    for query in (vq.w8a8_workspace_bytes, vq.gated_w8a8_workspace_bytes):
-        for m, k in ((0, 64), (32, 0), (32, 24), (32, 131072), (ROOM, 64)):
-            assert query(m, k) == 0
+    sizes = [vq.w8a8_workspace_bytes(n) for n in (1, 16, 17, 64, 65, 300, 1 << 24)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    for n in (0, -1, ROOM):
+        assert vq.w8a8_workspace_bytes(n) == 0
 
 
 def _norm(r=P[0], rdt=F32, y=P[1], ydt=BF16, post=P[2], gate=P[3], rows=0, alpha=1.0, w=P[4], eps=1e-6, ro=P[5],
