@@ -59,6 +59,18 @@ __device__ __forceinline__ float activate(float g, int kind) {
     return 0.5f * g * erfcf(g * -0.7071067811865476f);
 }
 
+// The 16-byte slot of a row in LDS that holds its first 16 bytes (XOR: the
+// others).  A 16-byte read of a wave takes four cycles of 16 lanes, the first two
+// {0-3, 12-15, 20-27} and {4-11, 16-19, 28-31}, the others 32 lanes on: with
+// lane = 16 g + row and slot = g ^ swizzle, each of these covers all 64 banks.
+template <int KC>
+__device__ __forceinline__ int swizzle(int row) {
+    if constexpr (KC == 128)
+        return row >> 1 & 7;  // two rows are 256 bytes
+    const int q = row >> 2 & 3;  // four rows are
+    return ((q ^ q >> 1) & 1) << 1 | q >> 1;  // 0, 2, 3, 1
+}
+
 // A piece of work: chunks [c0, c1) of one tile.
 struct Part {
     int tile, c0, c1;
@@ -110,10 +122,9 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
     };
 
     // Piece p = wave + kWaves i of a chunk holds rows kPieceRows p .. of it; a
-    // row's 16-byte slot s holds its bytes 16 (s ^ swizzle(row)) .. +16, where
-    // the swizzle counts rows of 256 bytes (all 64 banks)
+    // row's 16-byte slot s holds its bytes 16 (s ^ swizzle(row)) .. +16
     const int prow = lane / kSlots;
-    const int swz = KC == 128 ? 4 * (wave & 1) + (lane >> 4) : lane >> 4;
+    const int swz = swizzle<KC>(KC == 128 ? 8 * wave + prow : prow);
     const int byte16 = 16 * ((lane & (kSlots - 1)) ^ swz);
     const int voff = prow * K + byte16;
     rsrc_t rx, rw, ru;
@@ -159,8 +170,8 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
     };
 
     i32x4 acc[FT][RT];
-    u32x4 xb[kSteps][RT], wa[kSteps][FT];
-    const int sw = KC == 128 ? (j >> 1) & 7 : j >> 2;
+    u32x4 xb[RT], wa[FT];
+    const int sw = swizzle<KC>(j);
     const uint8_t *xs = lds + kWPieces * 1024 + (wr * RT * 16 + j) * KC;
     const uint8_t *ws = lds + (wf * FO * 16 + j) * KC;
     const auto read_x = [&](int s, int rt, int stage) {
@@ -344,9 +355,10 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
         return true;
     };
 
-    // The operands of a chunk are read while the one before it is multiplied:
-    // its stage is free from the next barrier on, and takes the chunk STAGES
-    // ahead.
+    // The operands of a step are read while the one before it is multiplied.
+    // The barrier comes before a chunk's last step: by then every wave holds
+    // the last operands of the chunk, whose stage takes the chunk STAGES ahead,
+    // and reads on in the next.
     open();
 #pragma unroll 1
     for (int s = 0; s < STAGES; ++s)
@@ -362,38 +374,38 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
                 acc[ft][rt] = i32x4{0, 0, 0, 0};
         // a part's first operands (again: nothing is held over the end of a part)
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
+        for (int ft = 0; ft < FT; ++ft)
+            wa[ft] = read_w(0, ft, stage);
 #pragma unroll
-            for (int ft = 0; ft < FT; ++ft)
-                wa[s][ft] = read_w(s, ft, stage);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                xb[s][rt] = read_x(s, rt, stage);
-        }
+        for (int rt = 0; rt < RT; ++rt)
+            xb[rt] = read_x(0, rt, stage);
         for (int c = p.c0; c < p.c1; ++c) {
-            landed(std::integral_constant<int, STAGES - 2>{});
-            issue(stage);
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-            u32x4 wn[kSteps][FT];
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
+            static_for<kSteps>([&](auto S) {
+                constexpr bool last = S.value == kSteps - 1;
+                if constexpr (last) {
+                    landed(std::integral_constant<int, STAGES - 2>{});
+                    issue(stage);
+                    stage = stage + 1 == STAGES ? 0 : stage + 1;
+                }
+                constexpr int next = last ? 0 : S.value + 1;
+                u32x4 wn[FT];
 #pragma unroll
                 for (int ft = 0; ft < FT; ++ft)
-                    wn[s][ft] = read_w(s, ft, stage);
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
+                    wn[ft] = read_w(next, ft, stage);
+                // (the scheduler would sink these reads to their uses)
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
                     for (int ft = 0; ft < FT; ++ft)
-                        acc[ft][rt] = mfma_i8(wa[s][ft], xb[s][rt], acc[ft][rt]);
-                    xb[s][rt] = read_x(s, rt, stage);
+                        acc[ft][rt] = mfma_i8(wa[ft], xb[rt], acc[ft][rt]);
+                    xb[rt] = read_x(next, rt, stage);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
                 for (int ft = 0; ft < FT; ++ft)
-                    wa[s][ft] = wn[s][ft];
+                    wa[ft] = wn[ft];
+            });
         }
         if (p.c1 - p.c0 == nch || join(p)) {
             int fb, rb;
@@ -470,7 +482,7 @@ hipError_t launch_rows(const W8A8Args &p) {
         return launch_shape<4, 2, 1, 4, 128, 4, GATED>(p);
     if (p.N <= 128)
         return launch_shape<4, 4, 2, 4, 64, 4, GATED>(p);
-    return launch_shape<8, 4, 2, 4, 64, 4, GATED>(p);
+    return launch_shape<8, 4, 2, 4, 128, 2, GATED>(p);
 }
 
 size_t slot_bytes(int n) {
