@@ -947,29 +947,58 @@ def kv_append(k, v, k_cache, v_cache, page_table, ctx_len, *, path=None, count=N
 
 # ---------------------------------------------------------------- the rest of a decoder layer
 
-def _here(*tensors):
-    """Refuses tensors of another device than the current one: the call's
-    kernels run there."""
-    dev = _torch()._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on the current device, cuda:%d" % dev)
+class _Args:
+    """Collects a call's contiguous arrays: checks each, gives its address, and
+    keeps its bytes' range, so that outputs can be refused that share memory
+    with another argument."""
+    def __init__(self):
+        self.dev, self.ranges = None, []
+
+    def on(self, t, name):
+        """Notes a tensor's device: all of a call's have to be on one."""
+        dev = t.get_device()
+        if self.dev is None and dev >= 0:
+            self.dev = dev
+        elif dev != self.dev:
+            raise ValueError("%s must be a device tensor, on the device of the others" % name)
+
+    def array(self, t, name, shape, dtype):
+        """Address of a contiguous array, or NULL for None."""
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous device tensor, %s %s" % (name, dtype, tuple(shape)))
+        self.on(t, name)
+        at = t.data_ptr()
+        self.ranges.append((at, at + t.nbytes, name))
+        return at
+
+    def here(self):
+        """Refuses tensors of another device than the current one, where the
+        kernels run."""
+        dev = _torch()._C._cuda_getDevice()
+        if dev != self.dev:
+            raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (self.dev, dev))
+
+    def apart(self, outputs, in_place=None):
+        """Refuses the last `outputs` arrays where one shares memory with any
+        other (except the pair of names `in_place`, which must be one array)."""
+        r = self.ranges
+        self.here()
+        for i in range(len(r) - outputs, len(r)):
+            lo, hi, name = r[i]
+            for j in range(i):
+                a, b, other = r[j]
+                if a < hi and lo < b and not (in_place == (name, other) and a == lo):
+                    raise ValueError("%s must not share memory with %s" % (name, other))
 
 
-def _span(t):
-    """First and one past the last byte of a tensor's elements."""
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
-    return t.data_ptr(), t.data_ptr() + last * t.element_size()
-
-
-def _apart(out, name: str, **inputs):
-    """Refuses an output that shares memory with another argument."""
-    lo, hi = _span(out)
-    for other, t in inputs.items():
-        if t is not None:
-            a, b = _span(t)
-            if a < hi and lo < b:
-                raise ValueError("%s must not share memory with %s" % (name, other))
+def _product_workspace(n, workspace, device, stream_handle):
+    """(pointer, bytes) for a product of 8-bit codes with n rows."""
+    if workspace is None:
+        return None, 0
+    ws = _sized_workspace("vq_w8a8_workspace_bytes", (n,), workspace, device, stream_handle)
+    return ws.ptr(), ws.tensor.numel()
 
 
 def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", stream=None):
@@ -987,25 +1016,17 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     N, K = x.shape
     M = w.shape[0]
     i8, f32 = torch.int8, torch.float32
-    _check_2d(out, "out", (N, M))
-    _here(w, w_scales, x, x_scales, bias, out)
-    _apart(out, "out", w=w, w_scales=w_scales, x=x, x_scales=x_scales, bias=bias)
+    a = _Args()
+    pw, pws = a.array(w, "w", (M, K), i8), a.array(w_scales, "w_scales", (M,), f32)
+    px, pxs = a.array(x, "x", (N, K), i8), a.array(x_scales, "x_scales", (N,), f32)
+    pb = a.array(bias, "bias", (M,), f32)
+    po = a.array(out, "out", (N, M), out.dtype)
+    a.apart(1)
     sh = _raw_stream(stream)
-    wp, wn = _w8a8_workspace(N, workspace, x.device, sh)
-    st = lib().vq_gemm_w8a8(_array(w, "w", (M, K), i8), _array(w_scales, "w_scales", (M,), f32),
-                            _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
-                            _array(bias, "bias", (M,), f32), _dev_ptr(out, "out"), _dtype_code(out), N, M, K, wp, wn,
-                            sh)
+    wp, wn = _product_workspace(N, workspace, x.device, sh)
+    st = lib().vq_gemm_w8a8(pw, pws, px, pxs, pb, po, _dtype_code(out), N, M, K, wp, wn, sh)
     _check(st, "vq_gemm_w8a8")
     return out
-
-
-def _w8a8_workspace(n, workspace, device, stream_handle):
-    """(pointer, bytes) for a product of 8-bit codes with n rows."""
-    if workspace is None:
-        return None, 0
-    ws = _sized_workspace("vq_w8a8_workspace_bytes", (n,), workspace, device, stream_handle)
-    return ws.ptr(), ws.nbytes
 
 
 def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activation: str = "silu", workspace="auto",
@@ -1024,16 +1045,16 @@ def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activa
     N, K = x.shape
     F = w_gate.shape[0]
     i8, f32 = torch.int8, torch.float32
-    _check_2d(out, "out", (N, F))
-    _here(w_gate, gate_scales, w_up, up_scales, x, x_scales, out)
-    _apart(out, "out", w_gate=w_gate, gate_scales=gate_scales, w_up=w_up, up_scales=up_scales, x=x,
-           x_scales=x_scales)
+    a = _Args()
+    pg, pgs = a.array(w_gate, "w_gate", (F, K), i8), a.array(gate_scales, "gate_scales", (F,), f32)
+    pu, pus = a.array(w_up, "w_up", (F, K), i8), a.array(up_scales, "up_scales", (F,), f32)
+    px, pxs = a.array(x, "x", (N, K), i8), a.array(x_scales, "x_scales", (N,), f32)
+    po = a.array(out, "out", (N, F), out.dtype)
+    a.apart(1)
     sh = _raw_stream(stream)
-    wp, wn = _w8a8_workspace(N, workspace, x.device, sh)
-    st = lib().vq_gated_w8a8(_array(w_gate, "w_gate", (F, K), i8), _array(gate_scales, "gate_scales", (F,), f32),
-                             _array(w_up, "w_up", (F, K), i8), _array(up_scales, "up_scales", (F,), f32),
-                             _array(x, "x", (N, K), i8), _array(x_scales, "x_scales", (N,), f32),
-                             ACTIVATIONS[activation], _dev_ptr(out, "out"), _dtype_code(out), N, F, K, wp, wn, sh)
+    wp, wn = _product_workspace(N, workspace, x.device, sh)
+    st = lib().vq_gated_w8a8(pg, pgs, pu, pus, px, pxs, ACTIVATIONS[activation], po, _dtype_code(out), N, F, K, wp, wn,
+                             sh)
     _check(st, "vq_gated_w8a8")
     return out
 
@@ -1061,33 +1082,32 @@ def residual_norm(residual, y=None, weight=None, *, out, scales_out=None, residu
     torch = _torch()
     if residual.dim() != 2:
         raise ValueError("residual must be [N][C]")
-    shape = N, C = tuple(residual.shape)
+    shape = N, C = residual.shape
     f32 = torch.float32
-    if y is None and (post_weight is not None or gate is not None or residual_out is not None):
-        raise ValueError("post_weight, gate and residual_out go with y")
-    if (out.dtype == torch.int8) != (scales_out is not None):
+    if y is None:
+        if post_weight is not None or gate is not None or residual_out is not None:
+            raise ValueError("post_weight, gate and residual_out go with y")
+        ydt, yc = None, 0
+    else:
+        ydt, yc = y.dtype, _dtype_code(y)
+        if yc != DTYPE_F16 and yc != DTYPE_BF16:
+            raise TypeError("y must be float16 or bfloat16")
+    oc = _dtype_code(out)
+    if (oc == DTYPE_I8) != (scales_out is not None):
         raise ValueError("scales_out goes with an int8 out")
-    if y is not None and y.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("y must be float16 or bfloat16")
     gate_rows = gate is not None and gate.dim() == 2
-    ydt = None if y is None else y.dtype
-    _here(residual, y, weight, out, scales_out, residual_out, post_weight, gate)
-    rest = dict(weight=weight, post_weight=post_weight, gate=gate, y=y)
-    _apart(out, "out", residual=residual, residual_out=residual_out, scales_out=scales_out, **rest)
-    if scales_out is not None:
-        _apart(scales_out, "scales_out", residual=residual, residual_out=residual_out, **rest)
-    if residual_out is not None:
-        same = residual_out.data_ptr() == residual.data_ptr()
-        _apart(residual_out, "residual_out", residual=None if same else residual, **rest)
-    st = lib().vq_residual_norm(
-        _array(residual, "residual", shape, residual.dtype), _dtype_code(residual), _array(y, "y", shape, ydt),
-        0 if y is None else _dtype_code(y), _array(post_weight, "post_weight", (C,), f32),
-        _array(gate, "gate", shape if gate_rows else (C,), ydt if gate_rows else f32), int(gate_rows), alpha,
-        _array(weight, "weight", (C,), f32), eps, _array(residual_out, "residual_out", shape, residual.dtype),
-        _array(out, "out", shape, out.dtype), _dtype_code(out), _array(scales_out, "scales_out", (N,), f32), N, C,
-        _raw_stream(stream))
+    a = _Args()
+    pr, py = a.array(residual, "residual", shape, residual.dtype), a.array(y, "y", shape, ydt)
+    pp = a.array(post_weight, "post_weight", (C,), f32)
+    pg = a.array(gate, "gate", shape if gate_rows else (C,), ydt if gate_rows else f32)
+    pw = a.array(weight, "weight", (C,), f32)
+    po, ps = a.array(out, "out", shape, out.dtype), a.array(scales_out, "scales_out", (N,), f32)
+    pro = a.array(residual_out, "residual_out", shape, residual.dtype)
+    a.apart(1 + (ps is not None) + (pro is not None), ("residual_out", "residual"))
+    st = lib().vq_residual_norm(pr, _dtype_code(residual), py, yc, pp, pg, gate_rows, alpha, pw, eps, pro, po, oc, ps,
+                                N, C, _raw_stream(stream))
     _check(st, "vq_residual_norm")
-    return out if scales_out is None else (out, scales_out)
+    return out if ps is None else (out, scales_out)
 
 
 def quant_rows_int8(x, q_out, scales_out, *, stream=None):
@@ -1099,12 +1119,12 @@ def quant_rows_int8(x, q_out, scales_out, *, stream=None):
     torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [N][K]")
-    N, K = x.shape
-    _here(x, q_out, scales_out)
-    _apart(q_out, "q_out", x=x, scales_out=scales_out)
-    _apart(scales_out, "scales_out", x=x)
-    st = lib().vq_quant_rows_int8(_dev_ptr(x, "x"), _dtype_code(x), _array(q_out, "q_out", (N, K), torch.int8),
-                                  _array(scales_out, "scales_out", (N,), torch.float32), N, K, _raw_stream(stream))
+    shape = N, K = x.shape
+    a = _Args()
+    px = a.array(x, "x", shape, x.dtype)
+    pq, ps = a.array(q_out, "q_out", shape, torch.int8), a.array(scales_out, "scales_out", (N,), torch.float32)
+    a.apart(2)
+    st = lib().vq_quant_rows_int8(px, _dtype_code(x), pq, ps, N, K, _raw_stream(stream))
     _check(st, "vq_quant_rows_int8")
     return q_out, scales_out
 
@@ -1127,53 +1147,70 @@ def rotate(q, k, inv_freq, ctx_len, *, tree_mask=None, interleaved: bool = False
         raise ValueError("q and k must be [batch][n][heads][head_dim]")
     shape = B, n, Hq, D = tuple(q.shape)
     dtype = q.dtype
-    if k is not None and k.dtype != dtype:
-        raise TypeError("q and k must have one dtype")
-    H = 0 if k is None else k.shape[2]
-    kv_shape = (B, n, H, D)
-    qs, ks = _rows(q, "q", shape), 0 if k is None else _rows(k, "k", kv_shape)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out goes with k")
+        H, kv_shape, ks = 0, None, 0
+    else:
+        if k.dtype != dtype:
+            raise TypeError("q and k must have one dtype")
+        H = k.shape[2]
+        kv_shape = (B, n, H, D)
+        ks = _rows(k, "k", kv_shape)
+    qs = _rows(q, "q", shape)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot_dim / 2]")
-    if k is None and k_out is not None:
-        raise ValueError("k_out goes with k")
-    _here(q, k, inv_freq, ctx_len, tree_mask, q_out, k_out)
+    half = inv_freq.shape[0]
+    a = _Args()
+    pf, pc = a.array(inv_freq, "inv_freq", (half,), torch.float32), a.array(ctx_len, "ctx_len", (B,), torch.int32)
+    pm = a.array(tree_mask, "tree_mask", (B, n), torch.int64)
+    for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")):
+        if t is not None:
+            a.on(t, name)
+    a.here()
     qos, kos = Hq * D, H * D
-    if q_out is not None:
-        qos = _turned_rows(q_out, "q_out", q, shape)
-    if k_out is not None:
-        kos = _turned_rows(k_out, "k_out", k, kv_shape)
     if q_out is not None or k_out is not None:
-        ins = {"q": (q, qs, Hq * D)} if k is None else {"q": (q, qs, Hq * D), "k": (k, ks, H * D)}
-        for name, out, so, width in (("q_out", q_out, qos, Hq * D), ("k_out", k_out, kos, H * D)):
-            if out is None:
-                continue
-            _apart(out, name, inv_freq=inv_freq, ctx_len=ctx_len, tree_mask=tree_mask)
-            for other, (t, stride, w) in ins.items():
-                in_place = other == name[0] and out.data_ptr() == t.data_ptr() and so == stride
-                if not in_place and _share_rows(out, so, width, t, stride, w):
-                    raise ValueError("%s must not share memory with %s (in place, the rows must be those of the input)"
-                                     % (name, other))
-        if q_out is not None and k_out is not None and _share_rows(q_out, qos, Hq * D, k_out, kos, H * D):
-            raise ValueError("q_out must not share memory with k_out")
+        qos, kos = _given_rows(a, q, qs, k, ks, q_out, k_out, shape, kv_shape)
     if q_out is None:
         q_out = _like(q, stream)
     if k is not None and k_out is None:
         k_out = _like(k, stream)
-    st = lib().vq_rotate(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, _dtype_code(q),
-                         _array(inv_freq, "inv_freq", (inv_freq.shape[0],), torch.float32),
-                         _array(ctx_len, "ctx_len", (B,), torch.int32),
-                         _array(tree_mask, "tree_mask", (B, n), torch.int64), q_out.data_ptr(), qos,
-                         None if k is None else k_out.data_ptr(), kos, B, n, Hq, H, D, 2 * inv_freq.shape[0],
-                         int(interleaved), scale, _raw_stream(stream))
+    st = lib().vq_rotate(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, _dtype_code(q), pf, pc, pm,
+                         q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos, B, n, Hq, H, D, 2 * half,
+                         interleaved, scale, _raw_stream(stream))
     _check(st, "vq_rotate")
     return q_out, k_out
 
 
-def _turned_rows(out, name, t, shape):
-    """Row stride of a given output of rotate."""
-    if out.dtype != t.dtype:
-        raise TypeError("%s must have the dtype of its input" % name)
-    return _rows(out, name, shape)
+def _given_rows(a, q, qs, k, ks, q_out, k_out, q_shape, k_shape):
+    """Row strides of rotate's outputs where they are given: each in place, or
+    apart from every argument."""
+    ins = [("q", q, qs, q_shape)] + ([("k", k, ks, k_shape)] if k is not None else [])
+    strides, seen = [q_shape[2] * q_shape[3], 0 if k is None else k_shape[2] * k_shape[3]], []
+    for at, (name, out) in enumerate((("q_out", q_out), ("k_out", k_out))):
+        if out is None:
+            continue
+        shape = ins[at][3]
+        if out.dtype != q.dtype:
+            raise TypeError("%s must have the dtype of its input" % name)
+        so = strides[at] = _rows(out, name, shape)
+        lo, hi = _span(out)
+        for b0, b1, other in a.ranges:
+            if b0 < hi and lo < b1:
+                raise ValueError("%s must not share memory with %s" % (name, other))
+        for other, t, stride, its in ins + seen:
+            in_place = other == name[0] and out.data_ptr() == t.data_ptr() and so == stride
+            if not in_place and _share_rows(out, so, shape[2] * shape[3], t, stride, its[2] * its[3]):
+                raise ValueError("%s must not share memory with %s (in place, the rows must be those of the input)"
+                                 % (name, other))
+        seen.append((name, out, so, shape))
+    return strides
+
+
+def _span(t):
+    """First and one past the last byte of a tensor's elements."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + last * t.element_size()
 
 
 def _share_rows(a, a_stride, a_width, b, b_stride, b_width):

@@ -48,13 +48,20 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 
 // The activations are written so that no large term is subtracted from
 // another: 0.5 g (1 + tanh z) = g / (1 + exp(-2 z)), and the Gaussian's
-// distribution function as 0.5 erfc(-g / sqrt 2).
+// distribution function as 0.5 erfc(-g / sqrt 2).  exp and the quotient are the
+// hardware's base-2 power and reciprocal (one unit each, two roundings beside
+// them): the product's rounding of g, three of them, moves the result by more.
+// An accurate exp and division took 11 us of a 256 x 128 tile, these 2.
+__device__ __forceinline__ float over_one_plus_exp2(float g, float t) {  // g / (1 + 2^t)
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+}
 __device__ __forceinline__ float activate(float g, int kind) {
+    constexpr float kLog2e = 1.4426950408889634f;
     if (kind == VQ_ACT_SILU)
-        return g / (1.0f + expf(-g));
+        return over_one_plus_exp2(g, -kLog2e * g);
     if (kind == VQ_ACT_GELU_TANH) {
-        const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-        return g / (1.0f + expf(-2.0f * z));
+        constexpr float kA = -2.0f * kLog2e * 0.7978845608028654f, kB = kA * 0.044715f;
+        return over_one_plus_exp2(g, g * __builtin_fmaf(kB * g, g, kA));
     }
     return 0.5f * g * erfcf(g * -0.7071067811865476f);
 }
@@ -423,23 +430,25 @@ struct Cut {
     int groups, whole, ranges;
 };
 
-int device_cus() {
-    static std::atomic<int> known[64];
+int current_device() {
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64)
-        return 256;
-    int n = known[dev].load(std::memory_order_relaxed);
+    return hipGetDevice(&dev) == hipSuccess && dev >= 0 ? dev : 64;
+}
+
+// Compute units of a device: the persistent workgroups of a launch, one each.
+int device_cus(int dev) {
+    static std::atomic<int> known[64];
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
-            n = 256;
+        if (dev >= 64 || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+            return 256;
         n = std::min(n, kMaxGroups);
         known[dev].store(n, std::memory_order_relaxed);
     }
     return n;
 }
 
-Cut cut_of(int64_t tiles, int nch, int most, bool pieces) {
-    const int G = device_cus();
+Cut cut_of(int64_t tiles, int nch, int most, bool pieces, int G) {
     const int64_t rem = tiles % G;
     if (!pieces || rem == 0)
         return Cut{(int)std::min<int64_t>(tiles, G), (int)tiles, 0};
@@ -454,17 +463,24 @@ hipError_t launch_shape(const W8A8Args &p) {
     constexpr int BM = 16 * RT * WR, BF = 16 * FT * WF, kOutFeats = GATED ? BF / 2 : BF;
     constexpr int kLds = STAGES * (BF + BM) * KC;
     const auto kern = w8a8_kernel<RT, FT, WR, WF, KC, STAGES, GATED>;
-    const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (e != hipSuccess)
-        return e;
+    static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much LDS
+    const int dev = current_device();
+    if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (e != hipSuccess)
+            return e;
+        if (dev < 64)
+            allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
+    const int cus = device_cus(dev);
     const int cols = (p.M + kOutFeats - 1) / kOutFeats, row_tiles = (p.N + BM - 1) / BM;
     const int nch = (p.K + KC - 1) / KC;
     const int per_launch = std::max(1, (1 << 30) / cols);  // row tiles per launch: tile numbers stay in 32 bits
-    const bool pieces = p.workspace && p.workspace_bytes >= kCounterBytes + (size_t)device_cus() * 2 * BM * BF * 4;
+    const bool pieces = p.workspace && p.workspace_bytes >= kCounterBytes + (size_t)cus * 2 * BM * BF * 4;
     for (int r0 = 0; r0 < row_tiles; r0 += per_launch) {
         const int rt = std::min(per_launch, row_tiles - r0);
-        const Cut cut = cut_of((int64_t)rt * cols, nch, 8, pieces);
+        const Cut cut = cut_of((int64_t)rt * cols, nch, 8, pieces, cus);
         KArgs a{p.w, p.up, p.x + (size_t)r0 * BM * p.K, p.w_scales, p.up_scales, p.x_scales + (size_t)r0 * BM, p.bias,
                 static_cast<char *>(p.out) + (size_t)r0 * BM * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2),
                 static_cast<uint32_t *>(p.workspace), std::min(p.N - r0 * BM, rt * BM), p.M, p.K, p.out_dtype,
@@ -491,7 +507,7 @@ size_t slot_bytes(int n) {
 
 }  // namespace
 
-size_t w8a8_workspace(int N) { return kCounterBytes + (size_t)device_cus() * 2 * slot_bytes(N); }
+size_t w8a8_workspace(int N) { return kCounterBytes + (size_t)device_cus(current_device()) * 2 * slot_bytes(N); }
 
 hipError_t launch_w8a8(const W8A8Args &p) { return p.up ? launch_rows<true>(p) : launch_rows<false>(p); }
 

@@ -141,12 +141,42 @@ def test_binding_refusals():
         vq.rotate(q, q.bfloat16(), f, f)
 
 
+def test_devices():
+    class T:
+        def __init__(self, dev):
+            self.get_device = lambda: dev
+    a = vq._Args()
+    with pytest.raises(ValueError, match="x must be a device tensor"):
+        a.on(T(-1), "x")
+    a.on(T(1), "x"), a.on(T(1), "y")
+    for dev in (-1, 0, 2):
+        with pytest.raises(ValueError, match="z must"):
+            a.on(T(dev), "z")
+
+
 def test_shared_memory_is_seen():
     t = torch.zeros(8, 64)
     assert vq._span(t[2:4]) == (t.data_ptr() + 512, t.data_ptr() + 1024)
+    a = vq._Args()
+    a.here = lambda: None
+
+    def ranges(*parts):
+        a.ranges = [(p.data_ptr(), p.data_ptr() + p.nbytes, name) for name, p in parts]
+    ranges(("x", t[3:]), ("out", t[2:4]))
+    with pytest.raises(ValueError, match="out must not share memory with x"):
+        a.apart(1)
+    ranges(("x", t[4:]), ("y", t[:2]), ("out", t[2:4]))
+    a.apart(1)
+    ranges(("x", t[:2]), ("y", t[2:4]), ("out", t[2:4]))
+    a.apart(1, ("out", "y"))
     with pytest.raises(ValueError, match="share"):
-        vq._apart(t[2:4], "out", x=t[3:])
-    vq._apart(t[2:4], "out", x=t[4:], y=t[:2], z=None)
+        a.apart(1, ("out", "x"))
+    ranges(("x", t[1:3]), ("out", t[2:4]))
+    with pytest.raises(ValueError, match="share"):
+        a.apart(1, ("out", "x"))
+    ranges(("x", t[4:]), ("one", t[:2]), ("two", t[1:4]))
+    with pytest.raises(ValueError, match="two must not share memory with one"):
+        a.apart(2)
     fused = torch.zeros(6, 96)
     a, b = fused[:, :64], fused[:, 64:]
     assert not vq._share_rows(a, 96, 64, b, 96, 32) and not vq._share_rows(b, 96, 32, a, 96, 64)
