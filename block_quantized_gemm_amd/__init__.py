@@ -1156,8 +1156,8 @@ def rotate(q, k, inv_freq, ctx_len, *, tree_mask=None, interleaved: bool = False
             raise TypeError("q and k must have one dtype")
         H = k.shape[2]
         kv_shape = (B, n, H, D)
-        ks = _rows(k, "k", kv_shape)
-    qs = _rows(q, "q", shape)
+        ks = _even_rows(k, "k", kv_shape)
+    qs = _even_rows(q, "q", shape)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot_dim / 2]")
     half = inv_freq.shape[0]
@@ -1172,14 +1172,24 @@ def rotate(q, k, inv_freq, ctx_len, *, tree_mask=None, interleaved: bool = False
     if q_out is not None or k_out is not None:
         qos, kos = _given_rows(a, q, qs, k, ks, q_out, k_out, shape, kv_shape)
     if q_out is None:
-        q_out = _like(q, stream)
+        q_out = q.new_empty(shape) if stream is None else _like(q, stream)
     if k is not None and k_out is None:
-        k_out = _like(k, stream)
+        k_out = k.new_empty(kv_shape) if stream is None else _like(k, stream)
     st = lib().vq_rotate(q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, _dtype_code(q), pf, pc, pm,
                          q_out.data_ptr(), qos, None if k is None else k_out.data_ptr(), kos, B, n, Hq, H, D, 2 * half,
                          interleaved, scale, _raw_stream(stream))
     _check(st, "vq_rotate")
     return q_out, k_out
+
+
+def _even_rows(t, name, shape):
+    """_rows of a tensor [batch][n][heads][dim], the usual slice of a fused
+    projection's output first."""
+    st = t.stride()
+    row, dim = st[1], shape[3]
+    if st == (shape[1] * row, row, dim, 1) and row >= shape[2] * dim and t.shape == shape:
+        return row
+    return _rows(t, name, shape)
 
 
 def _given_rows(a, q, qs, k, ks, q_out, k_out, q_shape, k_shape):

@@ -110,7 +110,7 @@ int vq_residual_norm(const void *residual, int residual_dtype, const void *y, in
     if (dev != VQ_OK)
         return dev;
     return status(vq::launch_row_norm({residual, residual_dtype, y, y_dtype, post_weight, gate, gate_rows != 0, alpha,
-                                       weight, false, eps, residual_out, out, out_dtype, scales_out, (int)n_rows,
+                                       weight, eps, residual_out, out, out_dtype, scales_out, (int)n_rows,
                                        (int)c, static_cast<hipStream_t>(stream)}));
 }
 
@@ -127,9 +127,8 @@ int vq_quant_rows_int8(const void *x, int x_dtype, int8_t *q_out, float *scales_
     const int dev = check_device();
     if (dev != VQ_OK)
         return dev;
-    return status(vq::launch_row_norm({x, x_dtype, nullptr, 0, nullptr, nullptr, false, 0.0f, nullptr, true, 0.0f,
-                                       nullptr, q_out, VQ_DTYPE_I8, scales_out, (int)n_rows, (int)k,
-                                       static_cast<hipStream_t>(stream)}));
+    return status(vq::launch_row_quant(x, x_dtype, q_out, scales_out, (int)n_rows, (int)k,
+                                       static_cast<hipStream_t>(stream)));
 }
 
 int vq_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int dtype, const float *inv_freq,

@@ -31,8 +31,7 @@ struct W8A8Args {
 hipError_t launch_w8a8(const W8A8Args &a);
 size_t w8a8_workspace(int N);  // for N rows of any product
 
-// Arguments of one residual update with its norms, or of a row quantization
-// (residual alone, no weight, raw: the rows as they are), already checked.
+// Arguments of one residual update with its norms, already checked.
 struct RowNormArgs {
     const void *residual;
     int residual_dtype;
@@ -43,7 +42,6 @@ struct RowNormArgs {
     bool gate_rows;  // gate [n][c] of y's type, else fp32 [c]
     float alpha;
     const float *weight;
-    bool raw;  // quantize the rows without a norm
     float eps;
     void *residual_out;  // or null
     void *out;
@@ -53,6 +51,7 @@ struct RowNormArgs {
     hipStream_t stream;
 };
 hipError_t launch_row_norm(const RowNormArgs &a);
+hipError_t launch_row_quant(const void *x, int x_dtype, int8_t *q, float *scales, int N, int C, hipStream_t stream);
 
 // Arguments of one rotation, already checked.
 struct RotateArgs {
