@@ -24,6 +24,7 @@ namespace vq {
 
 namespace {
 
+constexpr int KC = 128;  // k of a group's chunk: a 128-byte line of a row (half lines, 64 k, doubled the L2 requests)
 constexpr int kOutOfRange = 0x7FFFFFF0;  // past every range below: the load returns zeros
 constexpr int kCoherent = 0x10;          // sc1: agent-coherent, no cache maintenance needed
 constexpr int kMaxGroups = 512;          // persistent workgroups of a launch
@@ -66,16 +67,25 @@ __device__ __forceinline__ float activate(float g, int kind) {
     return 0.5f * g * erfcf(g * -0.7071067811865476f);
 }
 
-// The 16-byte slot of a row in LDS that holds its first 16 bytes (XOR: the
-// others).  A 16-byte read of a wave takes four cycles of 16 lanes, the first two
-// {0-3, 12-15, 20-27} and {4-11, 16-19, 28-31}, the others 32 lanes on: with
-// lane = 16 g + row and slot = g ^ swizzle, each of these covers all 64 banks.
-template <int KC>
-__device__ __forceinline__ int swizzle(int row) {
-    if constexpr (KC == 128)
-        return row >> 1 & 7;  // two rows are 256 bytes
-    const int q = row >> 2 & 3;  // four rows are
-    return ((q ^ q >> 1) & 1) << 1 | q >> 1;  // 0, 2, 3, 1
+// A wave's 16-byte LDS read takes four cycles of 16 lanes, the first two {0-3,
+// 12-15, 20-27} and {4-11, 16-19, 28-31}, the others 32 lanes on (seen in the
+// conflict counter).  Lane 16 g + j reads the 16 bytes 4 step + g of a row; two
+// rows are 256 bytes, all 64 banks.  The slots of a row are XORed with a number
+// that makes every cycle cover all banks once.
+//
+// Activations: lane j reads row j.
+__device__ __forceinline__ int swizzle_x(int row) { return row >> 1 & 7; }
+// Weights: which row of its wave's is feature j of tile ft.  In a pair of tiles
+// lane group g gets features 8 g .. 8 g + 7, so that a row of outputs leaves in
+// 16-byte pieces, 64 bytes side by side (4 and 32 made 134 MB of outputs take
+// 111 us).
+template <int FO>
+__device__ __forceinline__ int row_w(int ft, int j) {
+    return FO == 1 ? j : 32 * (ft >> 1) + 8 * (j >> 2) + 4 * (ft & 1) + (j & 3);
+}
+template <int FO>
+__device__ __forceinline__ int swizzle_w(int row) {
+    return FO == 1 ? row >> 1 & 7 : (row >> 3 & 3) << 1 | (row >> 1 & 1);
 }
 
 // A piece of work: chunks [c0, c1) of one tile.
@@ -83,27 +93,28 @@ struct Part {
     int tile, c0, c1;
 };
 
-// RT x FT tiles of 16 rows x 16 features per wave, WR x WF waves, chunks of KC
-// k in STAGES stages.
-template <int RT, int FT, int WR, int WF, int KC, int STAGES, bool GATED>
-__global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
+// RT x FT tiles of 16 rows x 16 features per wave, WR x WF waves that share
+// their operands, and WK such groups that share a tile's k: a chunk is WK
+// times KC = 128 k, group i's the i-th 128, in STAGES stages.
+template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED>
+__global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     constexpr int kWaves = WR * WF, BM = 16 * RT * WR, BF = 16 * FT * WF;
-    constexpr int kSlots = KC / 16, kPieceRows = 64 / kSlots;  // a wave loads pieces of 1 KiB: so many rows of KC bytes
-    constexpr int kWPieces = BF / kPieceRows, kXPieces = BM / kPieceRows, kPieces = kWPieces + kXPieces;
+    constexpr int kWPieces = BF / 8, kXPieces = BM / 8;  // 1 KiB each, a wave's load: 8 rows of KC bytes
+    constexpr int kPieces = kWPieces + kXPieces;
     constexpr int kPer = kPieces / kWaves, kExtra = kPieces % kWaves, kMost = kPer + (kExtra ? 1 : 0);
-    constexpr int kStage = kPieces * 1024;
+    constexpr int kStage = kPieces * 1024;  // of one group; each has its stages to itself
     constexpr int kOutFeats = GATED ? BF / 2 : BF;  // output features of the workgroup
     constexpr int FO = GATED ? FT / 2 : FT;         // output feature tiles of a wave
     constexpr int kSlot = BM * BF * 4;              // bytes of a tile's sums
     constexpr int kSteps = KC / 64;                 // MFMA steps of a chunk
-    static_assert(KC == 64 || KC == 128, "chunk");
-    static_assert(kWaves <= 8 && (KC == 64 || kWaves % 2 == 0) && (!GATED || FT % 2 == 0), "shape");
+    static_assert(WK * kWaves <= 8 && (kWaves == 1 || kWaves % 2 == 0) && (!GATED || FT % 2 == 0), "shape");
     static_assert(kWPieces % (GATED ? 2 * kWaves : kWaves) == 0, "a wave's i-th piece is of the same matrix in every wave");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wave = wave_id(), j = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+    const int wk = WK > 1 ? wave_id() / kWaves : 0, wave = WK > 1 ? wave_id() % kWaves : wave_id();
     const int wr = wave % WR, wf = wave / WR;
     const int G = (int)gridDim.x, me = xcd_run_index((int)blockIdx.x, G);
-    const int K = a.K, nch = (K + KC - 1) / KC;
+    const int K = a.K, nch = (K + WK * KC - 1) / (WK * KC);
     const int alone = a.whole / G + (me < a.whole % G ? 1 : 0);
     // the chunks after the whole tiles, in even ranges: mine are [u0, u1)
     const int R = (a.row_tiles * a.col_tiles - a.whole) * nch;
@@ -128,12 +139,20 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
         fb = (strip * kStrip + in % width) * kOutFeats;
     };
 
-    // Piece p = wave + kWaves i of a chunk holds rows kPieceRows p .. of it; a
-    // row's 16-byte slot s holds its bytes 16 (s ^ swizzle(row)) .. +16
-    const int prow = lane / kSlots;
-    const int swz = swizzle<KC>(KC == 128 ? 8 * wave + prow : prow);
-    const int byte16 = 16 * ((lane & (kSlots - 1)) ^ swz);
-    const int voff = prow * K + byte16;
+    // Piece p = wave + kWaves i of a group's chunk holds rows 8 p .. 8 p + 7 of
+    // it; a row's 16-byte slot s holds its bytes 16 (s ^ swizzle(row)) .. +16.
+    // The swizzles repeat every 32 rows (16 for the activations), with i.
+    constexpr int kWKinds = kWaves >= 4 ? 1 : 4 / kWaves, kXKinds = kWaves >= 2 ? 1 : 2;
+    const int prow = lane / 8;
+    int wvoff[kWKinds], xvoff[kXKinds], xbyte[kXKinds];
+#pragma unroll
+    for (int o = 0; o < kWKinds; ++o)
+        wvoff[o] = prow * K + 16 * ((lane & 7) ^ swizzle_w<FO>(8 * (wave + kWaves * o) + prow));
+#pragma unroll
+    for (int o = 0; o < kXKinds; ++o) {
+        xbyte[o] = 16 * ((lane & 7) ^ swizzle_x(8 * (wave + kWaves * o) + prow));
+        xvoff[o] = prow * K + xbyte[o];
+    }
     rsrc_t rx, rw, ru;
     int at = -1, lc = 0, lend = 0;  // the part whose chunks are being loaded
     const auto open = [&]() {
@@ -152,24 +171,27 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
         if constexpr (GATED)
             ru = make_rsrc(a.up + (size_t)fb * K, feats * (uint32_t)K);
     };
+    uint8_t *mem = lds + wk * STAGES * kStage;
     const auto issue = [&](int stage) {
-        const int k0 = max(lc, 0) * KC;
+        const int k0 = (max(lc, 0) * WK + wk) * KC;
         // past K the row's neighbour would be read: the activations are
         // zeros there, and so is the product
-        const int woff = lc < 0 ? kOutOfRange : voff;
-        const int xoff = k0 + byte16 < K ? woff : kOutOfRange;
-        uint8_t *st = lds + stage * kStage + wave * 1024;
-        const int step = kWaves * kPieceRows * K;  // a wave's next piece
-        const int base = wave * kPieceRows * K + k0;
+        const bool none = lc < 0 || k0 >= K;
+        uint8_t *st = mem + stage * kStage + wave * 1024;
+        const int step = kWaves * 8 * K;  // a wave's next piece
+        const int base = wave * 8 * K + k0;
         static_for<kMost>([&](auto I) {
             constexpr int i = I.value, x0 = kWPieces / kWaves, up0 = x0 / 2;
             if constexpr (i >= x0) {
+                constexpr int o = (i - x0) % kXKinds;
                 if (kExtra == 0 || i < kMost - 1 || wave < kExtra)
-                    bload16_lds(rx, st + 1024 * kWaves * i, xoff, base + (i - x0) * step);
+                    bload16_lds(rx, st + 1024 * kWaves * i, !none && k0 + xbyte[o] < K ? xvoff[o] : kOutOfRange,
+                                base + (i - x0) * step);
             } else if constexpr (GATED && i >= up0) {
-                bload16_lds(ru, st + 1024 * kWaves * i, woff, base + (i - up0) * step);
+                bload16_lds(ru, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[(i - up0) % kWKinds],
+                            base + (i - up0) * step);
             } else {
-                bload16_lds(rw, st + 1024 * kWaves * i, woff, base + i * step);
+                bload16_lds(rw, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[i % kWKinds], base + i * step);
             }
         });
         if (lc >= 0 && ++lc == lend)
@@ -178,22 +200,26 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
 
     i32x4 acc[FT][RT];
     u32x4 xb[RT], wa[FT];
-    const int sw = swizzle<KC>(j);
-    const uint8_t *xs = lds + kWPieces * 1024 + (wr * RT * 16 + j) * KC;
-    const uint8_t *ws = lds + (wf * FO * 16 + j) * KC;
+    const uint8_t *xs = mem + kWPieces * 1024 + (wr * RT * 16 + j) * KC, *ws = mem + wf * FO * 16 * KC;
     const auto read_x = [&](int s, int rt, int stage) {
-        return *reinterpret_cast<const u32x4 *>(xs + stage * kStage + rt * 16 * KC + 16 * ((4 * s + g) ^ sw));
+        return *reinterpret_cast<const u32x4 *>(xs + stage * kStage + rt * 16 * KC + 16 * ((4 * s + g) ^ swizzle_x(j)));
     };
     const auto read_w = [&](int s, int ft, int stage) {
-        return *reinterpret_cast<const u32x4 *>(ws + stage * kStage + (ft < FO ? ft * 16 : BF / 2 + (ft - FO) * 16) * KC +
-                                                16 * ((4 * s + g) ^ sw));
+        const int row = row_w<FO>(ft % FO, j);
+        return *reinterpret_cast<const u32x4 *>(ws + stage * kStage + ((ft < FO ? 0 : BF / 2) + row) * KC +
+                                                16 * ((4 * s + g) ^ swizzle_w<FO>(row)));
     };
-    const auto landed = [&](auto C) {  // all but the newest C chunks' loads
+    // All but the newest C chunks' loads have landed, and every wave that reads
+    // them holds what it read before.  A group of one wave waits for itself.
+    const auto landed = [&](auto C) {
         if (!kExtra || wave >= kExtra)
             wait_vmcnt<C.value * kPer>();
         else
             wait_vmcnt<C.value * kMost>();
-        lds_barrier();
+        if constexpr (kWaves == 1)
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        else
+            lds_barrier();
     };
 
     // Sums to outputs, in the accumulators' registers.
@@ -204,7 +230,7 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
             sx[rt] = __builtin_bit_cast(float, bload4<kAuxCached>(rs, 4 * (wr * RT * 16 + rt * 16 + j), 0));
-        const int f0 = fb + wf * FO * 16 + 4 * g;
+        const int f0 = fb + wf * FO * 16;
         if constexpr (GATED) {
             const rsrc_t rsu = make_rsrc(a.up_scales, (uint32_t)a.M * 4u);
             const auto all = [&](auto KIND) {
@@ -212,7 +238,7 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
                 for (int ft = 0; ft < FO; ++ft)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int o = 4 * (f0 + ft * 16 + r);
+                        const int o = 4 * (f0 + row_w<FO>(ft, 4 * g) + r);
                         const float sg = __builtin_bit_cast(float, bload4<kAuxCached>(rg, o, 0));
                         const float su = __builtin_bit_cast(float, bload4<kAuxCached>(rsu, o, 0));
 #pragma unroll
@@ -236,7 +262,7 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
             for (int ft = 0; ft < FT; ++ft)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int o = 4 * (f0 + ft * 16 + r);
+                    const int o = 4 * (f0 + row_w<FO>(ft, 4 * g) + r);
                     const float sg = __builtin_bit_cast(float, bload4<kAuxCached>(rg, o, 0));
                     // (-0 + y is y: no bias changes no bit)
                     const float add = biased ? __builtin_bit_cast(float, bload4<kAuxCached>(rb4, o, 0)) : -0.0f;
@@ -247,60 +273,57 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
         }
     };
     const auto store = [&](int fb, int rb) {
-        const int f0 = fb + wf * FO * 16 + 4 * g, n0 = rb + wr * RT * 16 + j;
-        const auto all = [&](auto OD, auto VEC) {
-            constexpr int esz = OD.value == VQ_DTYPE_F32 ? 4 : 2;
+        constexpr int kRun = FO == 1 ? 1 : 2;  // tiles whose values lie side by side in a row
+        const int f0 = fb + wf * FO * 16 + row_w<FO>(0, 4 * g), n0 = rb + wr * RT * 16 + j;
+        const auto all = [&](auto OD) {
+            constexpr int esz = OD.value == VQ_DTYPE_F32 ? 4 : 2, kWords = kRun * esz;
+            struct __attribute__((packed, aligned(esz))) Run {  // rows begin where M makes them begin
+                uint32_t w[kWords];
+            };
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const int n = n0 + rt * 16;
                 uint8_t *row = static_cast<uint8_t *>(a.out) + ((size_t)n * (size_t)a.M + (size_t)f0) * esz;
                 if (n < a.N) {
 #pragma unroll
-                    for (int ft = 0; ft < FO; ++ft) {
-                        float v[4];
+                    for (int q = 0; q < FO / kRun; ++q) {
+                        float v[4 * kRun];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int bits = acc[ft][rt][r];  // (a cast of the element itself reads element 0)
-                            v[r] = __builtin_bit_cast(float, bits);
+                        for (int e = 0; e < 4 * kRun; ++e) {
+                            const int bits = acc[kRun * q + e / 4][rt][e % 4];  // (a cast of the element reads element 0)
+                            v[e] = __builtin_bit_cast(float, bits);
                         }
-                        if constexpr (VEC.value) {
-                            if (f0 + ft * 16 < a.M) {
-                                if constexpr (OD.value == VQ_DTYPE_F32) {
-                                    *reinterpret_cast<f32x4 *>(row + ft * 64) = f32x4{v[0], v[1], v[2], v[3]};
-                                } else {
-                                    uint16_t h[4];
+                        const int left = a.M - (f0 + 32 * q);
+                        if (left >= 4 * kRun) {
+                            Run o;
 #pragma unroll
-                                    for (int r = 0; r < 4; ++r)
-                                        if constexpr (OD.value == VQ_DTYPE_BF16)
-                                            h[r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[r]));
-                                        else
-                                            h[r] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[r]));
-                                    *reinterpret_cast<u32x2 *>(row + ft * 32) =
-                                        u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
-                                }
+                            for (int e = 0; e < kWords; ++e) {
+                                if constexpr (OD.value == VQ_DTYPE_F32)
+                                    o.w[e] = __builtin_bit_cast(uint32_t, v[e]);
+                                else if constexpr (OD.value == VQ_DTYPE_BF16)
+                                    o.w[e] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e])) |
+                                             (uint32_t)__builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e + 1])) << 16;
+                                else
+                                    o.w[e] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e])) |
+                                             (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e + 1])) << 16;
                             }
+                            *reinterpret_cast<Run *>(row + 32 * q * esz) = o;
                         } else {
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (f0 + ft * 16 + r < a.M)
-                                    store_out(row, OD.value, ft * 16 + r, v[r]);
+                            for (int e = 0; e < 4 * kRun; ++e)
+                                if (e < left)
+                                    store_out(row, OD.value, 32 * q + e, v[e]);
                         }
                     }
                 }
             }
         };
-        const auto typed = [&](auto VEC) {
-            if (a.out_dtype == VQ_DTYPE_F32)
-                all(std::integral_constant<int, VQ_DTYPE_F32>{}, VEC);
-            else if (a.out_dtype == VQ_DTYPE_BF16)
-                all(std::integral_constant<int, VQ_DTYPE_BF16>{}, VEC);
-            else
-                all(std::integral_constant<int, VQ_DTYPE_F16>{}, VEC);
-        };
-        if (a.M % 4 == 0)  // 4 features of a row are aligned
-            typed(std::true_type{});
+        if (a.out_dtype == VQ_DTYPE_F32)
+            all(std::integral_constant<int, VQ_DTYPE_F32>{});
+        else if (a.out_dtype == VQ_DTYPE_BF16)
+            all(std::integral_constant<int, VQ_DTYPE_BF16>{});
         else
-            typed(std::false_type{});
+            all(std::integral_constant<int, VQ_DTYPE_F16>{});
     };
 
     // A tile cut between workgroups: each stores its sums, agent-coherent and
@@ -335,7 +358,7 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
             __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("" ::: "memory");
         // so many loads go out together, of kBatch workgroups' pieces or of a part of one
-        constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 8 ? kTiles : 8, kBatch = 8 / kAtOnce;
+        constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 16 ? kTiles : 16, kBatch = kTiles <= 8 ? 8 / kTiles : 1;
         for (int w0 = b0; w0 <= b1; w0 += kBatch) {
             static_for<kTiles / kAtOnce>([&](auto H) {
                 u32x4 v[kBatch][kAtOnce];
@@ -414,6 +437,29 @@ __global__ __launch_bounds__(64 * WR * WF) void w8a8_kernel(KArgs a) {
                     wa[ft] = wn[ft];
             });
         }
+        if constexpr (WK > 1) {
+            // the groups' sums, added by the first
+            i32x4 *red = reinterpret_cast<i32x4 *>(lds + WK * STAGES * kStage) + wave * FT * RT * 64 + lane;
+            constexpr int kGroup = kWaves * FT * RT * 64;
+            if (wk > 0)
+#pragma unroll
+                for (int ft = 0; ft < FT; ++ft)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        red[(wk - 1) * kGroup + (ft * RT + rt) * 64] = acc[ft][rt];
+            lds_barrier();
+            if (wk == 0)
+#pragma unroll
+                for (int k = 1; k < WK; ++k)
+#pragma unroll
+                    for (int ft = 0; ft < FT; ++ft)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            acc[ft][rt] += red[(k - 1) * kGroup + (ft * RT + rt) * 64];
+            lds_barrier();  // read before the next part's are written
+            if (wk > 0)
+                continue;
+        }
         if (p.c1 - p.c0 == nch || join(p)) {
             int fb, rb;
             place(p.tile, fb, rb);
@@ -458,11 +504,12 @@ Cut cut_of(int64_t tiles, int nch, int most, bool pieces, int G) {
     return Cut{whole ? G : ranges, whole, ranges};
 }
 
-template <int RT, int FT, int WR, int WF, int KC, int STAGES, bool GATED>
+template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED>
 hipError_t launch_shape(const W8A8Args &p) {
     constexpr int BM = 16 * RT * WR, BF = 16 * FT * WF, kOutFeats = GATED ? BF / 2 : BF;
-    constexpr int kLds = STAGES * (BF + BM) * KC;
-    const auto kern = w8a8_kernel<RT, FT, WR, WF, KC, STAGES, GATED>;
+    constexpr int kLds = WK * STAGES * (BF + BM) * KC + (WK - 1) * BM * BF * 4;
+    static_assert(kLds <= 160 * 1024, "LDS");
+    const auto kern = w8a8_kernel<RT, FT, WR, WF, WK, STAGES, GATED>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much LDS
     const int dev = current_device();
     if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
@@ -475,7 +522,7 @@ hipError_t launch_shape(const W8A8Args &p) {
     }
     const int cus = device_cus(dev);
     const int cols = (p.M + kOutFeats - 1) / kOutFeats, row_tiles = (p.N + BM - 1) / BM;
-    const int nch = (p.K + KC - 1) / KC;
+    const int nch = (p.K + WK * KC - 1) / (WK * KC);
     const int per_launch = std::max(1, (1 << 30) / cols);  // row tiles per launch: tile numbers stay in 32 bits
     const bool pieces = p.workspace && p.workspace_bytes >= kCounterBytes + (size_t)cus * 2 * BM * BF * 4;
     for (int r0 = 0; r0 < row_tiles; r0 += per_launch) {
@@ -485,7 +532,7 @@ hipError_t launch_shape(const W8A8Args &p) {
                 static_cast<char *>(p.out) + (size_t)r0 * BM * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2),
                 static_cast<uint32_t *>(p.workspace), std::min(p.N - r0 * BM, rt * BM), p.M, p.K, p.out_dtype,
                 p.activation, rt, cols, cut.whole, cut.ranges};
-        hipLaunchKernelGGL(kern, dim3(cut.groups), dim3(64 * WR * WF), kLds, p.stream, a);
+        hipLaunchKernelGGL(kern, dim3(cut.groups), dim3(64 * WR * WF * WK), kLds, p.stream, a);
     }
     return hipGetLastError();
 }
@@ -493,12 +540,12 @@ hipError_t launch_shape(const W8A8Args &p) {
 template <bool GATED>
 hipError_t launch_rows(const W8A8Args &p) {
     if (p.N <= 16)
-        return launch_shape<1, 2, 1, 4, 128, 6, GATED>(p);
+        return launch_shape<1, 2, 1, 4, 1, 6, GATED>(p);
     if (p.N <= 64)
-        return launch_shape<4, 2, 1, 4, 128, 4, GATED>(p);
+        return launch_shape<4, 2, 1, 4, 1, 4, GATED>(p);
     if (p.N <= 128)
-        return launch_shape<4, 4, 2, 4, 64, 4, GATED>(p);
-    return launch_shape<8, 4, 2, 4, 128, 2, GATED>(p);
+        return launch_shape<4, 4, 2, 4, 1, 3, GATED>(p);
+    return launch_shape<8, 4, 2, 4, 1, 2, GATED>(p);
 }
 
 size_t slot_bytes(int n) {
