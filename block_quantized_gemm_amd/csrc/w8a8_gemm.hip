@@ -38,8 +38,8 @@ struct KArgs {
     uint32_t *counters;  // and the pieces behind them
     int N, M, K, out_dtype, activation;
     int row_tiles, col_tiles;
-    int whole;   // tiles that every workgroup computes alone, in turn
-    int ranges;  // workgroups that share the chunks of the tiles after those
+    int whole;  // tiles that are computed whole, by the workgroups in turn
+    int cuts;   // each of the others is cut along k into so many pieces
 };
 
 __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
@@ -116,19 +116,20 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     const int G = (int)gridDim.x, me = xcd_run_index((int)blockIdx.x, G);
     const int K = a.K, nch = (K + WK * KC - 1) / (WK * KC);
     const int alone = a.whole / G + (me < a.whole % G ? 1 : 0);
-    // the chunks after the whole tiles, in even ranges: mine are [u0, u1)
-    const int R = (a.row_tiles * a.col_tiles - a.whole) * nch;
-    const int u0 = me < a.ranges ? (int)((int64_t)me * R / a.ranges) : 0;
-    const int u1 = me < a.ranges ? (int)((int64_t)(me + 1) * R / a.ranges) : 0;
-    const int first = u0 / nch;
-    const int parts = alone + (u1 > u0 ? (u1 - 1) / nch - first + 1 : 0);
+    // the tiles after the whole ones, cut: the workgroups of one XCD, whose
+    // numbers follow each other, work at the same k of neighbouring tiles
+    const int rest = a.row_tiles * a.col_tiles - a.whole;
+    const int parts = alone + (me < rest * a.cuts ? 1 : 0);
     if (parts == 0)
         return;
+    const auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };  // kept in a scalar register
+    const int my_cut = parts > alone ? uniform(me / rest) : 0;
+    const int my_c0 = parts > alone ? uniform(my_cut * nch / a.cuts) : 0;
+    const int my_c1 = parts > alone ? uniform((my_cut + 1) * nch / a.cuts) : 0;
     const auto part = [&](int i) -> Part {
         if (i < alone)
             return Part{i * G + me, 0, nch};
-        const int t = first + i - alone;
-        return Part{a.whole + t, max(u0 - t * nch, 0), min(u1 - t * nch, nch)};
+        return Part{a.whole + me - my_cut * rest, my_c0, my_c1};
     };
     // tiles in strips of kStrip feature columns, rows of a strip one after the
     // other: neighbours, which run on one XCD, share rows and columns in its L2
@@ -211,8 +212,11 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     };
     // All but the newest C chunks' loads have landed, and every wave that reads
     // them holds what it read before.  A group of one wave waits for itself.
+    int settled = 0;  // so many more chunks are known to have landed
     const auto landed = [&](auto C) {
-        if (!kExtra || wave >= kExtra)
+        if (settled > 0)
+            --settled;
+        else if (!kExtra || wave >= kExtra)
             wait_vmcnt<C.value * kPer>();
         else
             wait_vmcnt<C.value * kMost>();
@@ -331,15 +335,10 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     // wave: the waves of a tile's workgroups hold the same outputs.
     const auto join = [&](const Part &p) -> bool {
         const rsrc_t rp = make_rsrc(reinterpret_cast<uint8_t *>(a.counters) + kCounterBytes,
-                                    (uint32_t)a.ranges * 2u * (uint32_t)kSlot);
+                                    (uint32_t)(rest * a.cuts) * (uint32_t)kSlot);
         const int t = p.tile - a.whole;
-        const int b0 = (int)(((int64_t)(t * nch + 1) * a.ranges - 1) / R);
-        const int b1 = (int)(((int64_t)(t + 1) * nch * a.ranges - 1) / R);
-        const auto slot = [&](int who) {
-            const int begins = (int)((int64_t)who * R / a.ranges) / nch;  // the first tile of its range
-            return (2 * who + (begins == t ? 0 : 1)) * kSlot + wave * FT * RT * 1024;
-        };
-        const int mine = slot(me);
+        const auto slot = [&](int cut) { return (cut * rest + t) * kSlot + wave * FT * RT * 1024; };
+        const int mine = slot(my_cut);
 #pragma unroll
         for (int ft = 0; ft < FT; ++ft)
 #pragma unroll
@@ -352,20 +351,20 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         uint32_t old = 0;
         if (lane == 0)
             old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (__builtin_amdgcn_readfirstlane(old) != (uint32_t)(b1 - b0))
+        if (__builtin_amdgcn_readfirstlane(old) != (uint32_t)(a.cuts - 1))
             return false;
         if (lane == 0)  // every piece has arrived: the counter is ready for the next call
             __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         asm volatile("" ::: "memory");
         // so many loads go out together, of kBatch workgroups' pieces or of a part of one
-        constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 16 ? kTiles : 16, kBatch = kTiles <= 8 ? 8 / kTiles : 1;
-        for (int w0 = b0; w0 <= b1; w0 += kBatch) {
+        constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 16 ? kTiles : 8, kBatch = kTiles <= 8 ? 8 / kTiles : 1;
+        for (int w0 = 0; w0 < a.cuts; w0 += kBatch) {
             static_for<kTiles / kAtOnce>([&](auto H) {
                 u32x4 v[kBatch][kAtOnce];
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
                     const int who = w0 + q;
-                    const bool other = who <= b1 && who != me;
+                    const bool other = who < a.cuts && who != my_cut;
                     const int theirs = other ? slot(who) : 0;
                     const int off = other ? 16 * lane : kOutOfRange;
 #pragma unroll
@@ -464,17 +463,86 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
             int fb, rb;
             place(p.tile, fb, rb);
             finish(fb, rb);
+            // Loads and stores complete in order: what is in flight is waited
+            // for before the stores, so that the next chunks' waits do not
+            // wait for these (and the compiler need not for finish's loads).
+            wait_vmcnt<0>();
+            settled = STAGES - 1;
             store(fb, rb);
         }
     }
     wait_vmcnt<0>();  // loads past the last chunk write LDS: none outlives the workgroup
 }
 
-// How a launch cuts its tiles: `whole` of them by single workgroups, the rest
-// in `ranges` even ranges of chunks.  Without a workspace every tile is whole.
-struct Cut {
-    int groups, whole, ranges;
+// The forms of the kernel (template arguments and workgroups per CU) and what
+// each costs, in us: `begin` per launch, `chunk` per chunk of a workgroup,
+// `tile` per tile of a workgroup (its outputs), `join` + `piece` per piece where
+// tiles are cut; the weights' bytes at `hbm` TB/s, `again` of them for each
+// further row of tiles; all bytes into LDS at `l2` TB/s.  Fitted to 23,000
+// launches of 572 problems (1 to 4,093 rows, 128 to 17,408 features, k 256 to
+// 17,408, plain and gated).  The form with the least sum is launched: on those
+// problems it took 3% more than the best form in the mean and 1.3 times at
+// worst, where one form for each row count took up to twice the best.
+struct Form {
+    int rt, ft, wr, wf, wk, stages, per_cu;
+    float begin, chunk, tile, join, piece, hbm, again, l2;
+    constexpr int rows() const { return 16 * rt * wr; }
+    constexpr int feats() const { return 16 * ft * wf; }
 };
+constexpr Form kForms[] = {
+    {1, 2, 1, 1, 4, 3, 2, 5.2f, 0.24f, 1.0f, 1.4f, 0.12f, 6.2f, 0.10f, 18.f},  // 16 x 32
+    {2, 2, 1, 1, 4, 2, 2, 5.1f, 0.31f, 1.3f, 1.4f, 0.22f, 5.8f, 0.30f, 20.f},  // 32 x 32
+    {4, 2, 1, 2, 2, 3, 1, 5.1f, 0.44f, 1.9f, 1.7f, 0.44f, 5.8f, 0.36f, 18.f},  // 64 x 64
+    {4, 2, 2, 2, 1, 4, 1, 5.2f, 0.35f, 1.9f, 1.8f, 0.59f, 4.9f, 0.50f, 17.f},  // 128 x 64
+    {4, 2, 2, 4, 1, 4, 1, 5.4f, 0.48f, 2.5f, 3.0f, 0.72f, 5.1f, 0.52f, 15.f},  // 128 x 128
+    {8, 2, 2, 4, 1, 3, 1, 6.5f, 0.76f, 3.2f, 3.6f, 1.20f, 4.5f, 0.10f, 13.f},  // 256 x 128
+    {8, 4, 2, 4, 1, 2, 1, 5.1f, 1.34f, 7.9f, 5.4f, 2.35f, 2.8f, 0.29f, 10.f},  // 256 x 256
+};
+constexpr int kFormCount = sizeof(kForms) / sizeof(kForms[0]);
+
+// Forms whose tiles are at most half padding.
+bool fits_rows(const Form &f, int N) { return f.rows() == 16 || f.rows() < 2 * N; }
+
+int groups_of(const Form &f, int cus) { return std::min(cus * f.per_cu, kMaxGroups); }
+size_t pieces_bytes(const Form &f, int cus) {
+    return kCounterBytes + (size_t)groups_of(f, cus) * f.rows() * f.feats() * 4;
+}
+
+// How a launch cuts its tiles: `whole` of them by single workgroups, each of
+// the rest in `cuts` pieces.  Without room for the pieces every tile is whole.
+struct Plan {
+    int form, groups, whole, cuts;
+};
+
+Plan plan_of(const W8A8Args &p, bool gated, int cus) {
+    Plan best{};
+    float least = 0.f;
+    for (int i = 0; i < kFormCount; ++i) {
+        const Form &f = kForms[i];
+        if (!fits_rows(f, p.N))
+            continue;
+        const int G = groups_of(f, cus), feats = gated ? f.feats() / 2 : f.feats();
+        const int64_t rows = (p.N + f.rows() - 1) / f.rows(), cols = (p.M + feats - 1) / feats, tiles = rows * cols;
+        const int nch = (p.K + f.wk * KC - 1) / (f.wk * KC), rest = (int)(tiles % G);
+        const bool room = p.workspace && p.workspace_bytes >= pieces_bytes(f, cus);
+        const float weights = (float)p.M * (float)p.K * (gated ? 2.f : 1.f) * (1.f + f.again * (float)(rows - 1));
+        const float moved = (float)tiles * (float)nch * (float)((f.rows() + f.feats()) * f.wk * KC);
+        const float bytes = std::max(weights / (f.hbm * 1e6f), moved / (f.l2 * 1e6f));
+        const int most = rest && room ? std::min({G / rest, nch, 12}) : 1;
+        for (int cuts = 1; cuts <= most; ++cuts) {
+            const float whole = (float)(cuts == 1 ? (tiles + G - 1) / G : tiles / G) * (float)nch;
+            const float chunks = whole + (cuts == 1 ? 0.f : (float)((nch + cuts - 1) / cuts));
+            const float us = f.begin + std::max(f.chunk * chunks, bytes) + f.tile * (float)((tiles + G - 1) / G) +
+                             (cuts == 1 ? 0.f : f.join + f.piece * (float)cuts);
+            if (best.groups == 0 || us < least) {
+                least = us;
+                best = cuts == 1 ? Plan{i, (int)std::min<int64_t>(tiles, G), (int)tiles, 0}
+                                 : Plan{i, tiles > G ? G : rest * cuts, (int)(tiles - rest), cuts};
+            }
+        }
+    }
+    return best;
+}
 
 int current_device() {
     int dev = 0;
@@ -494,24 +562,14 @@ int device_cus(int dev) {
     return n;
 }
 
-Cut cut_of(int64_t tiles, int nch, int most, bool pieces, int G) {
-    const int64_t rem = tiles % G;
-    if (!pieces || rem == 0)
-        return Cut{(int)std::min<int64_t>(tiles, G), (int)tiles, 0};
-    // a tile is cut into `most` pieces at most
-    const int ranges = (int)std::min<int64_t>({(int64_t)G, rem * nch, rem * most});
-    const int whole = (int)(tiles - rem);
-    return Cut{whole ? G : ranges, whole, ranges};
-}
-
-template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED>
-hipError_t launch_shape(const W8A8Args &p) {
-    constexpr int BM = 16 * RT * WR, BF = 16 * FT * WF, kOutFeats = GATED ? BF / 2 : BF;
-    constexpr int kLds = WK * STAGES * (BF + BM) * KC + (WK - 1) * BM * BF * 4;
-    static_assert(kLds <= 160 * 1024, "LDS");
-    const auto kern = w8a8_kernel<RT, FT, WR, WF, WK, STAGES, GATED>;
+template <int I, bool GATED>
+hipError_t launch_form(const W8A8Args &p, const Plan &plan, int dev) {
+    constexpr Form f = kForms[I];
+    constexpr int BM = f.rows(), BF = f.feats(), kOutFeats = GATED ? BF / 2 : BF;
+    constexpr int kLds = f.wk * f.stages * (BF + BM) * KC + (f.wk - 1) * BM * BF * 4;
+    static_assert(kLds * f.per_cu <= 160 * 1024, "LDS");
+    const auto kern = w8a8_kernel<f.rt, f.ft, f.wr, f.wf, f.wk, f.stages, GATED>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much LDS
-    const int dev = current_device();
     if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -520,41 +578,51 @@ hipError_t launch_shape(const W8A8Args &p) {
         if (dev < 64)
             allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
     }
-    const int cus = device_cus(dev);
-    const int cols = (p.M + kOutFeats - 1) / kOutFeats, row_tiles = (p.N + BM - 1) / BM;
-    const int nch = (p.K + WK * KC - 1) / (WK * KC);
-    const int per_launch = std::max(1, (1 << 30) / cols);  // row tiles per launch: tile numbers stay in 32 bits
-    const bool pieces = p.workspace && p.workspace_bytes >= kCounterBytes + (size_t)cus * 2 * BM * BF * 4;
-    for (int r0 = 0; r0 < row_tiles; r0 += per_launch) {
-        const int rt = std::min(per_launch, row_tiles - r0);
-        const Cut cut = cut_of((int64_t)rt * cols, nch, 8, pieces, cus);
-        KArgs a{p.w, p.up, p.x + (size_t)r0 * BM * p.K, p.w_scales, p.up_scales, p.x_scales + (size_t)r0 * BM, p.bias,
-                static_cast<char *>(p.out) + (size_t)r0 * BM * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2),
-                static_cast<uint32_t *>(p.workspace), std::min(p.N - r0 * BM, rt * BM), p.M, p.K, p.out_dtype,
-                p.activation, rt, cols, cut.whole, cut.ranges};
-        hipLaunchKernelGGL(kern, dim3(cut.groups), dim3(64 * WR * WF * WK), kLds, p.stream, a);
-    }
+    const KArgs a{p.w, p.up, p.x, p.w_scales, p.up_scales, p.x_scales, p.bias, p.out,
+                  static_cast<uint32_t *>(p.workspace), p.N, p.M, p.K, p.out_dtype, p.activation,
+                  (p.N + BM - 1) / BM, (p.M + kOutFeats - 1) / kOutFeats, plan.whole, plan.cuts};
+    hipLaunchKernelGGL(kern, dim3(plan.groups), dim3(64 * f.wr * f.wf * f.wk), kLds, p.stream, a);
     return hipGetLastError();
 }
 
-template <bool GATED>
-hipError_t launch_rows(const W8A8Args &p) {
-    if (p.N <= 16)
-        return launch_shape<1, 2, 1, 4, 1, 6, GATED>(p);
-    if (p.N <= 64)
-        return launch_shape<4, 2, 1, 4, 1, 4, GATED>(p);
-    if (p.N <= 128)
-        return launch_shape<4, 4, 2, 4, 1, 3, GATED>(p);
-    return launch_shape<8, 4, 2, 4, 1, 2, GATED>(p);
+template <bool GATED, int I = 0>
+hipError_t launch_plan(const W8A8Args &p, const Plan &plan, int dev) {
+    if constexpr (I + 1 < kFormCount)
+        if (plan.form != I)
+            return launch_plan<GATED, I + 1>(p, plan, dev);
+    return launch_form<I, GATED>(p, plan, dev);
 }
 
-size_t slot_bytes(int n) {
-    return n <= 16 ? 16 * 128 * 4 : n <= 64 ? 64 * 128 * 4 : n <= 128 ? 128 * 256 * 4 : 256 * 256 * 4;
+// Rows per launch: the tile numbers of a launch stay in 32 bits.
+template <bool GATED>
+hipError_t launch_rows(W8A8Args p) {
+    const int dev = current_device(), cus = device_cus(dev);
+    const int64_t cols = (p.M + 15) / 16;
+    const int most = (int)std::min<int64_t>(VQ_MAX_DIM, std::max<int64_t>(256, ((int64_t)1 << 30) / cols / 16 * 256));
+    const int N = p.N;
+    for (int n0 = 0; n0 < N; n0 += most) {
+        W8A8Args part = p;
+        part.x += (size_t)n0 * p.K;
+        part.x_scales += n0;
+        part.out = static_cast<char *>(p.out) + (size_t)n0 * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2);
+        part.N = std::min(most, N - n0);
+        const hipError_t e = launch_plan<GATED>(part, plan_of(part, GATED, cus), dev);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
-size_t w8a8_workspace(int N) { return kCounterBytes + (size_t)device_cus(current_device()) * 2 * slot_bytes(N); }
+size_t w8a8_workspace(int N) {
+    const int cus = device_cus(current_device());
+    size_t need = 0;
+    for (const Form &f : kForms)
+        if (fits_rows(f, N))
+            need = std::max(need, pieces_bytes(f, cus));
+    return need;
+}
 
 hipError_t launch_w8a8(const W8A8Args &p) { return p.up ? launch_rows<true>(p) : launch_rows<false>(p); }
 
