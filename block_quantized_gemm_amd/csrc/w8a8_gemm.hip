@@ -475,14 +475,15 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
 }
 
 // The forms of the kernel (template arguments and workgroups per CU) and what
-// each costs, in us: `begin` per launch, `chunk` per chunk of a workgroup,
-// `tile` per tile of a workgroup (its outputs), `join` + `piece` per piece where
-// tiles are cut; the weights' bytes at `hbm` TB/s, `again` of them for each
-// further row of tiles; all bytes into LDS at `l2` TB/s.  Fitted to 23,000
-// launches of 572 problems (1 to 4,093 rows, 128 to 17,408 features, k 256 to
-// 17,408, plain and gated).  The form with the least sum is launched: on those
-// problems it took 3% more than the best form in the mean and 1.3 times at
-// worst, where one form for each row count took up to twice the best.
+// each costs, in us: `begin` per launch, `tile` per tile of a workgroup (its
+// outputs), `join` + `piece` per piece where tiles are cut, and each round of
+// workgroups the longest of three: `chunk` per chunk, the bytes into LDS at
+// `l2` TB/s, its share of the weights at `hbm` TB/s, `again` of them for each
+// further row of tiles.  Fitted to 11,000 launches of 870 problems (1 to 4,093
+// rows, 128 to 17,408 features, k 256 to 17,408, plain and gated).  The form with
+// the least sum is launched: on those problems it took 2% more than the best one
+// in the mean and 1.4 times at worst (a 7 us launch); one form for each row
+// count took up to twice the best.
 struct Form {
     int rt, ft, wr, wf, wk, stages, per_cu;
     float begin, chunk, tile, join, piece, hbm, again, l2;
@@ -490,13 +491,15 @@ struct Form {
     constexpr int feats() const { return 16 * ft * wf; }
 };
 constexpr Form kForms[] = {
-    {1, 2, 1, 1, 4, 3, 2, 5.2f, 0.24f, 1.0f, 1.4f, 0.12f, 6.2f, 0.10f, 18.f},  // 16 x 32
-    {2, 2, 1, 1, 4, 2, 2, 5.1f, 0.31f, 1.3f, 1.4f, 0.22f, 5.8f, 0.30f, 20.f},  // 32 x 32
-    {4, 2, 1, 2, 2, 3, 1, 5.1f, 0.44f, 1.9f, 1.7f, 0.44f, 5.8f, 0.36f, 18.f},  // 64 x 64
-    {4, 2, 2, 2, 1, 4, 1, 5.2f, 0.35f, 1.9f, 1.8f, 0.59f, 4.9f, 0.50f, 17.f},  // 128 x 64
-    {4, 2, 2, 4, 1, 4, 1, 5.4f, 0.48f, 2.5f, 3.0f, 0.72f, 5.1f, 0.52f, 15.f},  // 128 x 128
-    {8, 2, 2, 4, 1, 3, 1, 6.5f, 0.76f, 3.2f, 3.6f, 1.20f, 4.5f, 0.10f, 13.f},  // 256 x 128
-    {8, 4, 2, 4, 1, 2, 1, 5.1f, 1.34f, 7.9f, 5.4f, 2.35f, 2.8f, 0.29f, 10.f},  // 256 x 256
+    {1, 2, 1, 1, 4, 3, 2, 5.0f, 0.25f, 1.0f, 1.0f, 0.16f, 6.3f, 0.34f, 18.6f},  // 16 x 32
+    {1, 2, 1, 4, 1, 6, 1, 5.2f, 0.26f, 1.0f, 1.3f, 0.21f, 6.2f, 0.24f, 14.6f},  // 16 x 128
+    {2, 2, 1, 1, 4, 2, 2, 5.2f, 0.34f, 1.0f, 1.0f, 0.28f, 4.3f, 0.07f, 19.3f},  // 32 x 32
+    {4, 2, 1, 2, 2, 3, 1, 5.0f, 0.41f, 2.0f, 1.1f, 0.48f, 5.9f, 0.43f, 18.7f},  // 64 x 64
+    {4, 2, 1, 4, 1, 4, 1, 4.9f, 0.36f, 1.9f, 1.6f, 0.51f, 6.0f, 0.34f, 16.3f},  // 64 x 128
+    {4, 2, 2, 2, 1, 4, 1, 5.0f, 0.34f, 1.9f, 1.4f, 0.62f, 4.7f, 0.64f, 17.7f},  // 128 x 64
+    {4, 2, 2, 4, 1, 4, 1, 5.2f, 0.46f, 2.4f, 2.8f, 0.68f, 5.0f, 0.39f, 15.7f},  // 128 x 128
+    {8, 2, 2, 4, 1, 3, 1, 6.0f, 0.74f, 3.3f, 3.3f, 1.19f, 5.0f, 0.50f, 13.5f},  // 256 x 128
+    {8, 4, 2, 4, 1, 2, 1, 6.8f, 1.28f, 5.1f, 6.7f, 2.35f, 4.0f, 0.10f, 10.6f},  // 256 x 256
 };
 constexpr int kFormCount = sizeof(kForms) / sizeof(kForms[0]);
 
@@ -525,14 +528,16 @@ Plan plan_of(const W8A8Args &p, bool gated, int cus) {
         const int64_t rows = (p.N + f.rows() - 1) / f.rows(), cols = (p.M + feats - 1) / feats, tiles = rows * cols;
         const int nch = (p.K + f.wk * KC - 1) / (f.wk * KC), rest = (int)(tiles % G);
         const bool room = p.workspace && p.workspace_bytes >= pieces_bytes(f, cus);
-        const float weights = (float)p.M * (float)p.K * (gated ? 2.f : 1.f) * (1.f + f.again * (float)(rows - 1));
-        const float moved = (float)tiles * (float)nch * (float)((f.rows() + f.feats()) * f.wk * KC);
-        const float bytes = std::max(weights / (f.hbm * 1e6f), moved / (f.l2 * 1e6f));
+        const float weights = (float)p.M * (float)p.K * (gated ? 2.f : 1.f) * (1.f + f.again * (float)(rows - 1)) /
+                              (f.hbm * 1e6f * (float)tiles);  // us for a tile's share of them
+        const float chunk = (float)((f.rows() + f.feats()) * f.wk * KC) / (f.l2 * 1e6f);  // us for a chunk into LDS
+        const auto round = [&](int chunks, int groups, float tiles_in) {
+            return std::max({f.chunk * (float)chunks, chunk * (float)chunks * (float)groups, weights * tiles_in});
+        };
+        const float fixed = f.begin + f.tile * (float)((tiles + G - 1) / G) + (float)(tiles / G) * round(nch, G, (float)G);
         const int most = rest && room ? std::min({G / rest, nch, 12}) : 1;
         for (int cuts = 1; cuts <= most; ++cuts) {
-            const float whole = (float)(cuts == 1 ? (tiles + G - 1) / G : tiles / G) * (float)nch;
-            const float chunks = whole + (cuts == 1 ? 0.f : (float)((nch + cuts - 1) / cuts));
-            const float us = f.begin + std::max(f.chunk * chunks, bytes) + f.tile * (float)((tiles + G - 1) / G) +
+            const float us = fixed + (rest ? round((nch + cuts - 1) / cuts, rest * cuts, (float)rest) : 0.f) +
                              (cuts == 1 ? 0.f : f.join + f.piece * (float)cuts);
             if (best.groups == 0 || us < least) {
                 least = us;
