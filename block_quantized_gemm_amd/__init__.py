@@ -968,7 +968,8 @@ class _Args:
             return None
         if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
             raise ValueError("%s must be a contiguous device tensor, %s %s" % (name, dtype, tuple(shape)))
-        self.on(t, name)
+        if t.get_device() != self.dev:
+            self.on(t, name)
         at = t.data_ptr()
         self.ranges.append((at, at + t.nbytes, name))
         return at

@@ -96,7 +96,8 @@ struct Part {
 // RT x FT tiles of 16 rows x 16 features per wave, WR x WF waves that share
 // their operands, and WK such groups that share a tile's k: a chunk is WK
 // times KC = 128 k, group i's the i-th 128, in STAGES stages.
-template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED>
+// AUX: the cache policy of the weights' loads.
+template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED, int AUX>
 __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     constexpr int kWaves = WR * WF, BM = 16 * RT * WR, BF = 16 * FT * WF;
     constexpr int kWPieces = BF / 8, kXPieces = BM / 8;  // 1 KiB each, a wave's load: 8 rows of KC bytes
@@ -173,7 +174,9 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
             ru = make_rsrc(a.up + (size_t)fb * K, feats * (uint32_t)K);
     };
     uint8_t *mem = lds + wk * STAGES * kStage;
-    const auto issue = [&](int stage) {
+    // Loads of the chunk that comes next, kMost pieces of 1 KiB a wave: [I0, I1)
+    // of them.
+    const auto load = [&](int stage, auto I0, auto I1) {
         const int k0 = (max(lc, 0) * WK + wk) * KC;
         // past K the row's neighbour would be read: the activations are
         // zeros there, and so is the product
@@ -181,20 +184,22 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         uint8_t *st = mem + stage * kStage + wave * 1024;
         const int step = kWaves * 8 * K;  // a wave's next piece
         const int base = wave * 8 * K + k0;
-        static_for<kMost>([&](auto I) {
-            constexpr int i = I.value, x0 = kWPieces / kWaves, up0 = x0 / 2;
+        static_for<I1.value - I0.value>([&](auto I) {
+            constexpr int i = I0.value + I.value, x0 = kWPieces / kWaves, up0 = x0 / 2;
             if constexpr (i >= x0) {
                 constexpr int o = (i - x0) % kXKinds;
                 if (kExtra == 0 || i < kMost - 1 || wave < kExtra)
                     bload16_lds(rx, st + 1024 * kWaves * i, !none && k0 + xbyte[o] < K ? xvoff[o] : kOutOfRange,
                                 base + (i - x0) * step);
             } else if constexpr (GATED && i >= up0) {
-                bload16_lds(ru, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[(i - up0) % kWKinds],
+                bload16_lds<AUX>(ru, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[(i - up0) % kWKinds],
                             base + (i - up0) * step);
             } else {
-                bload16_lds(rw, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[i % kWKinds], base + i * step);
+                bload16_lds<AUX>(rw, st + 1024 * kWaves * i, none ? kOutOfRange : wvoff[i % kWKinds], base + i * step);
             }
         });
+    };
+    const auto loaded = [&]() {  // on to the next chunk
         if (lc >= 0 && ++lc == lend)
             open();
     };
@@ -390,8 +395,10 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     // and reads on in the next.
     open();
 #pragma unroll 1
-    for (int s = 0; s < STAGES; ++s)
-        issue(s);
+    for (int s = 0; s < STAGES; ++s) {
+        load(s, std::integral_constant<int, 0>{}, std::integral_constant<int, kMost>{});
+        loaded();
+    }
     landed(std::integral_constant<int, STAGES - 1>{});
     int stage = 0;
     for (int i = 0; i < parts; ++i) {
@@ -411,9 +418,9 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         for (int c = p.c0; c < p.c1; ++c) {
             static_for<kSteps>([&](auto S) {
                 constexpr bool last = S.value == kSteps - 1;
+                const int free = stage;
                 if constexpr (last) {
                     landed(std::integral_constant<int, STAGES - 2>{});
-                    issue(stage);
                     stage = stage + 1 == STAGES ? 0 : stage + 1;
                 }
                 constexpr int next = last ? 0 : S.value + 1;
@@ -423,14 +430,21 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
                     wn[ft] = read_w(next, ft, stage);
                 // (the scheduler would sink these reads to their uses)
                 __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
+                static_for<RT>([&](auto R) {
+                    constexpr int rt = R.value;
 #pragma unroll
                     for (int ft = 0; ft < FT; ++ft)
                         acc[ft][rt] = mfma_i8(wa[ft], xb[rt], acc[ft][rt]);
                     xb[rt] = read_x(next, rt, stage);
+                    // a part of the loads between the matrix instructions: all at
+                    // once they fill the address unit's queue and stop the wave
+                    if constexpr (last)
+                        load(free, std::integral_constant<int, rt * kMost / RT>{},
+                             std::integral_constant<int, (rt + 1) * kMost / RT>{});
                     __builtin_amdgcn_sched_barrier(0);
-                }
+                });
+                if constexpr (last)
+                    loaded();
 #pragma unroll
                 for (int ft = 0; ft < FT; ++ft)
                     wa[ft] = wn[ft];
@@ -567,13 +581,13 @@ int device_cus(int dev) {
     return n;
 }
 
-template <int I, bool GATED>
+template <int I, bool GATED, int AUX>
 hipError_t launch_form(const W8A8Args &p, const Plan &plan, int dev) {
     constexpr Form f = kForms[I];
     constexpr int BM = f.rows(), BF = f.feats(), kOutFeats = GATED ? BF / 2 : BF;
     constexpr int kLds = f.wk * f.stages * (BF + BM) * KC + (f.wk - 1) * BM * BF * 4;
     static_assert(kLds * f.per_cu <= 160 * 1024, "LDS");
-    const auto kern = w8a8_kernel<f.rt, f.ft, f.wr, f.wf, f.wk, f.stages, GATED>;
+    const auto kern = w8a8_kernel<f.rt, f.ft, f.wr, f.wf, f.wk, f.stages, GATED, AUX>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much LDS
     if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
@@ -595,7 +609,15 @@ hipError_t launch_plan(const W8A8Args &p, const Plan &plan, int dev) {
     if constexpr (I + 1 < kFormCount)
         if (plan.form != I)
             return launch_plan<GATED, I + 1>(p, plan, dev);
-    return launch_form<I, GATED>(p, plan, dev);
+    // One row of tiles reads the weights once.  They are loaded past the caches
+    // where the 256 MB behind them could not keep them for the next call beside
+    // the rest of a layer (178 MB, 16 rows: 40.7 us, 43.3 with the caches), and
+    // through them where it could (42 MB, one row, three matrices in turn: 10.3
+    // us, 11.1 past them).
+    if constexpr (kForms[I].rows() == 16)
+        if ((int64_t)p.M * p.K * (GATED ? 2 : 1) >= (int64_t)128 << 20)
+            return launch_form<I, GATED, kAuxStream>(p, plan, dev);
+    return launch_form<I, GATED, kAuxCached>(p, plan, dev);
 }
 
 // Rows per launch: the tile numbers of a launch stay in 32 bits.
