@@ -995,11 +995,28 @@ class _Args:
 
 
 def _product_workspace(n, workspace, device, stream_handle):
-    """(pointer, bytes) for a product of 8-bit codes with n rows."""
+    """(pointer, bytes) for a product of 8-bit codes with n rows.  A cached
+    workspace is not made while a graph is captured: its zero fill would run with
+    the graph's replays only, and eager calls share it.  The captured call then
+    runs without one (the same bits)."""
     if workspace is None:
         return None, 0
-    ws = _sized_workspace("vq_w8a8_workspace_bytes", (n,), workspace, device, stream_handle)
-    return ws.ptr(), ws.tensor.numel()
+    query = "vq_w8a8_workspace_bytes"
+    if workspace == "auto":
+        need = _ws_needs.get((query, n))
+        if need is None:
+            need = _ws_needs[(query, n)] = w8a8_workspace_bytes(n)
+        ws = _auto_ws.get((query, device, stream_handle))
+        if ws is None or ws.nbytes < need:
+            if _torch().cuda.is_current_stream_capturing():
+                return None, 0
+            ws = _auto_workspace((query, device, stream_handle), need, device)
+    elif isinstance(workspace, Workspace):
+        ws = workspace
+    else:
+        raise TypeError("workspace must be a Workspace, None or 'auto'")
+    ws.used_on(stream_handle)
+    return ws.ptr(), ws.nbytes
 
 
 def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", stream=None):
@@ -1009,8 +1026,8 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     [N], as quant_rows_int8 and residual_norm write them; bias: float32 [M] or
     None; out: float16 / bfloat16 / float32 [N][M].  The integer sums are exact:
     a row's bits do not depend on the other rows.  workspace: "auto" (a cached
-    one per device and stream), a Workspace, or None (a slower form, the same
-    bits)."""
+    one per device and stream; while a graph is captured, only one that an
+    earlier call made), a Workspace, or None (a slower form, the same bits)."""
     torch = _torch()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N][K] and w [M][K]")

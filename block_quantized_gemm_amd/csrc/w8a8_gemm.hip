@@ -10,11 +10,28 @@
 // number and the split of K.
 //
 // A workgroup computes BM rows x BF features with the 16x16x64 int8 MFMA,
-// weights as the first operand: a lane then holds 4 consecutive features of
-// one row, and in the gated form gate and up of the same feature.  Chunks of
-// 128 k are loaded straight into LDS, `STAGES - 1` chunks ahead; 16-byte pieces
-// are XOR-swizzled by row so that the operand reads of 16 rows cover all 64
-// banks.
+// weights as the first operand: a lane then holds runs of consecutive features
+// of one row, and in the gated form gate and up of the same feature.  Chunks
+// of 128 k go straight into LDS, up to STAGES of them in flight or in use; the
+// operands of a step are read while the one before it is multiplied.
+//
+// Persistent workgroups, one or two a CU: whole rounds of tiles first, then the
+// tiles that are left, each cut along k into as many equal pieces as there are
+// workgroups for (the last piece to arrive adds the others).  Equal pieces keep
+// the workgroups of an XCD at the same k of neighbouring tiles, whose operands
+// then meet in L2: even ranges over all chunks balance better on paper and
+// took 313 us where whole tiles on 240 of 256 CUs took 210.
+//
+// Nine forms, chosen by their estimated time (kForms).  For few rows, groups of
+// waves split a tile's k and each streams for itself, without barriers: 1 row
+// 8192 to 5120 in 10 us (4.2 TB/s), 16 rows 5120 to 17408 in 20.5 us (4.4 TB/s, a
+// copy reaches 4.9), 16 rows gated 17408 in 41 us; bound by the weights' bytes
+// and 5 us of launch, first loads and last stores.  For many, 256 x 256 tiles:
+// 4,093 rows 17408 to 5120 in 294 us (2,479 TOPS), 4,096 rows to 8192 in 437 us
+// (2,670; hipBLASLt's int8 product of 8192^3 2,458), gated 2,048 rows in 316 us.
+// There the matrix instructions run 65% of the time: without the loads the loop
+// takes 328 of 437 us, with loads that all hit L2 392, without LDS reads either
+// 293.
 #include <atomic>
 
 #include "layer_internal.h"
@@ -28,7 +45,11 @@ constexpr int KC = 128;  // k of a group's chunk: a 128-byte line of a row (half
 constexpr int kOutOfRange = 0x7FFFFFF0;  // past every range below: the load returns zeros
 constexpr int kCoherent = 0x10;          // sc1: agent-coherent, no cache maintenance needed
 constexpr int kMaxGroups = 512;          // persistent workgroups of a launch
-constexpr size_t kCounterBytes = kMaxGroups * 8 * 4;  // a tile cut between workgroups: one counter per wave
+// A tile cut between workgroups has one arrival counter per wave, at zero
+// between calls; the pieces begin where the verify GEMMs' do, so that a
+// workspace shared with them keeps their counters too.
+constexpr size_t kCounterBytes = 64 * 1024;
+static_assert(kMaxGroups * 8 * 4 <= kCounterBytes, "counters");
 constexpr int kStrip = 4;                // feature columns of tiles walked together
 
 struct KArgs {
@@ -273,11 +294,11 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
                 for (int r = 0; r < 4; ++r) {
                     const int o = 4 * (f0 + row_w<FO>(ft, 4 * g) + r);
                     const float sg = __builtin_bit_cast(float, bload4<kAuxCached>(rg, o, 0));
-                    // (-0 + y is y: no bias changes no bit)
+                    // (y + -0 is y: no bias changes no bit)
                     const float add = biased ? __builtin_bit_cast(float, bload4<kAuxCached>(rb4, o, 0)) : -0.0f;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
-                        acc[ft][rt][r] = __builtin_bit_cast(int, (float)acc[ft][rt][r] * sx[rt] * sg + add);
+                        acc[ft][rt][r] = __builtin_bit_cast(int, __builtin_fmaf((float)acc[ft][rt][r] * sx[rt], sg, add));
                 }
         }
     };

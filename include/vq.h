@@ -654,8 +654,8 @@ int vq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_strid
  *   bias      fp32 [M] or NULL
  *   out       [N][M], out_dtype F16, BF16 or F32
  * The sum is an exact 32-bit integer; it is converted to fp32, multiplied by
- * the row's scale, then by the channel's, the bias added, and the result
- * rounded to out_dtype: each of these one fp32 operation.  Output bits are
+ * the row's scale, then by the channel's with the bias added in one FMA, and the
+ * result rounded to out_dtype: each of these one fp32 operation.  Output bits are
  * therefore the same for any N, any neighbouring rows, with and without a
  * workspace and on every device.
  * Sizes: 1 <= N, M <= VQ_MAX_DIM; 16 <= K <= VQ_MAX_W8A8_K, K % 16 == 0.
@@ -748,10 +748,12 @@ int vq_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, 
               int interleaved, float scale, void *stream);
 
 /* Workspace bytes of the two products for n_rows rows, whatever M and K (0
- * for n_rows outside the limits; on an MI355X 4 MiB for a draft block of 16
- * rows, 128 MiB for prompts).  As for the verify GEMMs: zero-filled once by the
+ * for n_rows outside the limits; on an MI355X 2 MiB for a draft block of 16
+ * rows, 64 MiB for prompts).  As for the verify GEMMs: zero-filled once by the
  * caller, left ready for the next call, not shared by calls that overlap in
- * time; NULL or a smaller one runs a slower form. */
+ * time; NULL or a smaller one runs a slower form.  It may be shared with the
+ * verify GEMMs, but not with the operators whose workspace holds any contents
+ * (greedy and tree verification, tree attention). */
 size_t vq_w8a8_workspace_bytes(int64_t n_rows);
 
 /*
