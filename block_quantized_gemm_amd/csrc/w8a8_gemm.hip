@@ -28,7 +28,7 @@
 // copy reaches 4.9), 16 rows gated 17408 in 41 us; bound by the weights' bytes
 // and 5 us of launch, first loads and last stores.  For many, 256 x 256 tiles:
 // 4,093 rows 17408 to 5120 in 294 us (2,479 TOPS), 4,096 rows to 8192 in 437 us
-// (2,670; hipBLASLt's int8 product of 8192^3 2,458), gated 2,048 rows in 316 us.
+// (2,670; the library int8 product of 8192^3 2,458), gated 2,048 rows in 316 us.
 // There the matrix instructions run 65% of the time: without the loads the loop
 // takes 328 of 437 us, with loads that all hit L2 392, without LDS reads either
 // 293.

@@ -135,3 +135,18 @@ def test_binding_checks():
             vq.rotate(**(dict(q=q, k=k, inv_freq=f, ctx_len=c) | bad))
     with pytest.raises(vq.VqError):
         vq.rotate(q, k, f[:4].contiguous(), c)
+
+
+def test_offsets_past_32_bits():
+    """Rows 8,000 elements apart in a fused matrix of 4.8 10^9 elements."""
+    B, n, d = 3, 200000, 64
+    m = torch.zeros(B, n, 8000, dtype=torch.float16, device="cuda")
+    m[2, -1] = torch.randn(8000, generator=torch.Generator().manual_seed(1)).half().cuda()
+    q, k = m[..., 7000:7064].unflatten(-1, (1, d)), m[..., 7872:8000].unflatten(-1, (2, d))
+    freq = _freq(64)
+    ctx = np.array([1, 2, 50], np.int32)
+    qo, ko = vq.rotate(q, k, torch.from_numpy(freq).cuda(), torch.from_numpy(ctx).cuda())
+    assert not qo[:2].any() and not ko[2, :-1].any()
+    pos = np.array([[50 + n - 1]])
+    _check(qo[2:, -1:], q[2:, -1:], pos, freq, False, 1.0, "f16")
+    _check(ko[2:, -1:], k[2:, -1:], pos, freq, False, 1.0, "f16")

@@ -158,3 +158,20 @@ def test_binding_checks():
             vq.residual_norm(r, **(dict(y=y, weight=w, out=out, residual_out=ro) | bad))
     with pytest.raises(TypeError):
         vq.quant_rows_int8(r.double(), torch.empty(4, 64, dtype=torch.int8, device="cuda"), w[:4].clone())
+
+
+def test_offsets_past_32_bits():
+    n, c = 140000, 32768
+    x = torch.zeros(n, c, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 65535, 131071, 131072, n - 1]
+    gen = torch.Generator().manual_seed(8)
+    for r in rows:
+        x[r] = torch.randn(c, generator=gen).to(torch.bfloat16).cuda()
+    q, s = vq.quant_rows_int8(x, torch.empty(n, c, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda"))
+    want_q, want_s = R.quant(x[rows].float().cpu().numpy())
+    assert np.array_equal(s[rows].cpu().numpy(), want_s) and np.array_equal(q[rows].cpu().numpy(), want_q)
+    assert not q[1].any() and not q[n - 2].any()
+    out = torch.empty_like(x)
+    vq.residual_norm(x, out=out)
+    _, _, h, eh = R.norm(_np(x[rows]), None, None, None, None, 1.0, float(np.float32(1e-6)))
+    _within(out[rows], h, eh, "bf16")

@@ -165,3 +165,19 @@ def test_binding_checks():
         vq.gemm_w8a8(dw, dws, dx, dxs, dw.view(-1)[:512].view(torch.float32).view(4, 32))
     with pytest.raises(vq.VqError):
         vq.gemm_w8a8(dw[:, :24].contiguous(), dws, dx[:, :24].contiguous(), dxs, out)
+
+
+@pytest.mark.parametrize("n,m,k", [(300007, 21, 32), (3, 400009, 64), (70001, 70000, 16)])
+def test_many_rows_and_features(n, m, k):
+    """Long sides, and outputs whose offsets pass 32 bits: sampled rows and columns."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (m, k), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.ones(max(n, m), device="cuda")
+    out = vq.gemm_w8a8(w, one[:m], x, one[:n], torch.empty(n, m, dtype=torch.bfloat16, device="cuda"))
+    rows = torch.tensor(sorted({0, 1, n // 2, n - 2 if n > 1 else 0, n - 1}), device="cuda")
+    cols = torch.tensor(sorted({0, m // 3, m - 1, m - 2}), device="cuda")
+    want = x[rows].double() @ w.double().t().contiguous()  # whole numbers below 2^24: one rounding to bf16
+    assert torch.equal(out[rows], want.to(torch.bfloat16))
+    want = x.double() @ w[cols].double().t().contiguous()
+    assert torch.equal(out[:, cols], want.to(torch.bfloat16))
