@@ -181,3 +181,71 @@ def test_many_rows_and_features(n, m, k):
     assert torch.equal(out[rows], want.to(torch.bfloat16))
     want = x.double() @ w[cols].double().t().contiguous()
     assert torch.equal(out[:, cols], want.to(torch.bfloat16))
+
+
+# (rows, features, k): on 256 compute units these reach every form of the
+# kernel, with tiles whole, in several rounds, and cut in two, three and more
+PLAIN = [(1, 33, 4144), (1, 1485, 5696), (17, 16889, 1568), (18, 16883, 4112), (17, 17435, 144), (17, 22395, 3728),
+         (17, 17401, 5072), (18, 6885, 144), (18, 17067, 224), (1178, 65, 8720), (935, 33, 7584), (33, 11535, 144),
+         (34, 5279, 6928), (98, 2633, 6240), (66, 8215, 144), (131, 16677, 144), (227, 2101, 4176), (325, 5405, 144),
+         (716, 5381, 144), (199, 3949, 7488), (99, 4359, 4624), (66, 16807, 144), (257, 17083, 144), (66, 9273, 6352),
+         (269, 15471, 5680), (68, 8359, 5680), (264, 11209, 8224), (134, 21853, 144), (653, 22055, 144), (199, 8507, 5312),
+         (258, 22397, 144), (401, 8333, 7056), (1300, 6001, 1040)]
+GATED = [(1, 33, 4144), (1, 16453, 400), (1, 737, 5728), (1, 17125, 5936), (1, 16469, 4192), (1, 8195, 144),
+         (17, 18887, 1680), (18, 17485, 1648), (19, 3387, 144), (17, 8903, 224), (1284, 35, 8000), (615, 33, 7200),
+         (33, 5449, 144), (36, 21099, 2272), (33, 3273, 5584), (99, 1307, 6736), (66, 4223, 144), (35, 16503, 144),
+         (33, 21095, 1936), (163, 1375, 4144), (33, 16975, 1888), (1219, 773, 144), (1273, 1609, 208), (193, 1935, 8048),
+         (66, 19033, 1968), (101, 2085, 4752), (69, 16559, 1952), (66, 8215, 144), (66, 16807, 144), (67, 4561, 5776),
+         (65, 21137, 3120), (194, 2155, 3728), (67, 19055, 3040), (133, 11069, 144), (258, 22397, 144), (577, 13061, 1936),
+         (197, 4155, 5424), (386, 17053, 2016), (131, 16677, 144), (517, 17321, 144), (386, 4313, 6816)]
+
+
+def _device_case(n, m, k):
+    g = torch.Generator(device="cuda").manual_seed(n * 31 + m + k)
+    x, w = (torch.randint(-128, 128, (r, k), generator=g, device="cuda", dtype=torch.int8) for r in (n, m))
+    xs = 0.01 * torch.exp(torch.randn(n, generator=g, device="cuda"))
+    return x, xs, w, 0.02 / k ** 0.5 * torch.exp(torch.randn(m, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("n,m,k", PLAIN)
+def test_every_form(n, m, k):
+    """The definition's own operations, bit for bit: the exact sum, to fp32,
+    times the row's scale, times the channel's; twice, so that the counters of
+    cut tiles are seen to be back at zero, and without a workspace."""
+    x, xs, w, ws = _device_case(n, m, k)
+    dots = x.double() @ w.double().t().contiguous()  # exact in 64 bits
+    want = dots.float() * xs[:, None] * ws
+    for out, workspace in (("f32", "auto"), ("bf16", "auto"), ("f16", None)):
+        got = vq.gemm_w8a8(w, ws, x, xs, torch.full((n, m), float("nan"), dtype=DT[out], device="cuda"),
+                           workspace=workspace)
+        assert torch.equal(got, want.to(DT[out])), out
+
+
+@pytest.mark.parametrize("n,f,k", GATED)
+def test_every_gated_form(n, f, k):
+    """The rows as the form for few rows gives them, which the tests above hold
+    to the definition, bit for bit; and the definition in 64 bits."""
+    x, xs, w, ws = _device_case(n, 2 * f, k)
+    act = ["silu", "gelu", "gelu_tanh"][(n + f) % 3]
+
+    def call(rows, workspace="auto"):
+        return vq.gated_w8a8(w[:f], ws[:f], w[f:], ws[f:], x[rows], xs[rows],
+                             torch.full((len(xs[rows]), f), float("nan"), device="cuda"), activation=act,
+                             workspace=workspace)
+    whole = call(slice(None))
+    assert torch.equal(whole, call(slice(None))) and torch.equal(whole, call(slice(None), None))
+    for at in range(0, n, max(16, n // 6 // 16 * 16)):
+        assert torch.equal(whole[at:at + 16], call(slice(at, at + 16))), at
+    # the sum before the scales: it is an integer, 0 where the terms cancel
+    both = (x.double() @ w.double().t().contiguous()) * xs.double()[:, None] * ws.double()
+    g, u = both[:, :f], both[:, f:]
+    if act == "silu":
+        want = g * torch.sigmoid(g) * u
+    elif act == "gelu":
+        want = 0.5 * g * torch.special.erfc(g * -0.5 ** 0.5) * u
+    else:
+        z = (2 / np.pi) ** 0.5 * (g + 0.044715 * g ** 3)
+        want = g * torch.sigmoid(2 * z) * u
+    # sums of 1.1 |g| 3 U, 3 U of u and the activation's own (R.activate), the largest of the three kinds
+    bound = R.U * (3.4 * g.abs() * u.abs() + (60 + 24 * g.abs() ** 3 + 4 * g * g) * want.abs()) + 1e-37 * (1 + u.abs())
+    assert bool(((whole.double() - want).abs() <= bound).all())
