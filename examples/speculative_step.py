@@ -1,6 +1,6 @@
 """Speculative decoding with a tree of drafted tokens, on random weights:
 
-    python examples/speculative_step.py [--steps 8] [--batch 4] [--nodes 16]
+    python examples/speculative_step.py [--steps 8] [--batch 4] [--nodes 16] [--weights q4_0|int8]
 
 A small transformer (attention and a Q4_0 projection on each side of it, no
 MLP) generates with a bigram table as its drafter.  One step, all of it on the
@@ -14,6 +14,19 @@ device and without a host synchronisation:
   vq.gemm_q4_0          logits of every node
   vq.tree_verify        the accepted path and the next token, from random numbers
   vq.kv_append          the accepted nodes' keys and values, all layers at once
+
+With --weights int8 the layers are whole decoder layers in 8 bits, positions
+and a gated feed-forward block included:
+
+  per layer
+    vq.residual_norm    the update from the layer before, its norm, rows to 8 bits
+    vq.gemm_w8a8        queries, keys and values
+    vq.rotate           at every node's position in its tree, in place
+    vq.tree_attention
+    vq.quant_rows_int8, vq.gemm_w8a8      back to the hidden width
+    vq.residual_norm
+    vq.gated_w8a8       both projections, the activation and the product
+    vq.quant_rows_int8, vq.gemm_w8a8
 """
 from __future__ import annotations
 
@@ -67,6 +80,63 @@ class Model:
             x = x + self._matmul(self.back[i], seen.view(B * n, -1))
             keys[i], values[i] = k, v
         return self._matmul(self.head, x.contiguous()).view(B, n, -1), keys, values
+
+
+class Int8Model(Model):
+    """Random 8-bit weights of decoder layers: attention with rotary positions
+    and a gated feed-forward block, a norm before each."""
+
+    def __init__(self, layers=2, hidden=512, q_heads=8, kv_heads=2, dim=64, ffn=1392, vocab=512, seed=0, device="cuda"):
+        super().__init__(layers, hidden, q_heads, kv_heads, dim, vocab, seed, device)
+        self.ffn = ffn
+        g = torch.Generator().manual_seed(seed + 1)
+
+        def int8(m, k):  # codes uniform, scales so that a row of unit inputs gives about a unit output
+            codes = torch.randint(-127, 128, (m, k), generator=g, dtype=torch.int8)
+            return codes.to(self.device), torch.full((m,), 1.0 / 73.0 / k ** 0.5, device=self.device)
+
+        self.qkv = [int8((q_heads + 2 * kv_heads) * dim, hidden) for _ in range(layers)]
+        self.back = [int8(hidden, q_heads * dim) for _ in range(layers)]
+        self.both = [int8(2 * ffn, hidden) for _ in range(layers)]  # the gate's rows, then the other factor's
+        self.down = [int8(hidden, ffn) for _ in range(layers)]
+        self.head = int8(vocab, hidden)
+        self.norms = [(1.0 + 0.1 * torch.randn(hidden, generator=g)).to(self.device) for _ in range(2 * layers + 1)]
+        half = torch.arange(dim // 2, dtype=torch.float64)
+        self.inv_freq = (1e4 ** (-2.0 * half / dim)).to(torch.float32).to(self.device)
+
+    def _new(self, *shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device=self.device)
+
+    def _norm(self, x, y, weight):
+        """x += y, and the norm of the sum as 8-bit rows and their scales."""
+        out, scales = self._new(*x.shape, dtype=torch.int8), self._new(x.shape[0], dtype=torch.float32)
+        return vq.residual_norm(x, y, weight, out=out, scales_out=scales, residual_out=None if y is None else x)
+
+    def _quant(self, x):
+        return vq.quant_rows_int8(x, self._new(*x.shape, dtype=torch.int8), self._new(x.shape[0], dtype=torch.float32))
+
+    def _product(self, w, rows):
+        return vq.gemm_w8a8(w[0], w[1], rows[0], rows[1], self._new(rows[0].shape[0], w[0].shape[0]))
+
+    def forward(self, tokens, cache, tree_mask=None):
+        B, n = tokens.shape
+        f = self.ffn
+        x, y = self.embedding[tokens.long().view(-1)].float(), None
+        keys = self._new(self.layers, B, n, self.kv_heads, self.dim)
+        values = torch.empty_like(keys)
+        widths = [self.q_heads * self.dim, self.kv_heads * self.dim, self.kv_heads * self.dim]
+        for i in range(self.layers):
+            rows = self._product(self.qkv[i], self._norm(x, y, self.norms[2 * i])).view(B, n, -1)
+            q, k, v = (t.unflatten(-1, (-1, self.dim)) for t in torch.split(rows, widths, dim=-1))
+            vq.rotate(q, k, self.inv_freq, cache.lens, tree_mask=tree_mask, q_out=q, k_out=k)
+            seen = vq.tree_attention(q, k, v, cache.k[i], cache.v[i], cache.table, cache.lens, tree_mask=tree_mask)
+            y = self._product(self.back[i], self._quant(seen.view(B * n, -1)))
+            h, hs = self._norm(x, y, self.norms[2 * i + 1])
+            (w, ws), g = self.both[i], self._new(B * n, f)
+            vq.gated_w8a8(w[:f], ws[:f], w[f:], ws[f:], h, hs, g)
+            y = self._product(self.down[i], self._quant(g))
+            keys[i], values[i] = k, v
+        return self._product(self.head, self._norm(x, y, self.norms[-1])).view(B, n, -1), keys, values
 
 
 class Cache:
@@ -134,8 +204,9 @@ def main():
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--nodes", type=int, default=16)
     ap.add_argument("--prompt", type=int, default=40)
+    ap.add_argument("--weights", choices=("q4_0", "int8"), default="q4_0")
     args = ap.parse_args()
-    model = Model()
+    model = Model() if args.weights == "q4_0" else Int8Model()
     cache = Cache(model, args.batch, args.prompt + args.steps * args.nodes)
     g = torch.Generator(device=model.device)
     g.manual_seed(1)
