@@ -42,7 +42,7 @@ namespace vq {
 namespace {
 
 constexpr int KC = 128;  // k of a group's chunk: a 128-byte line of a row (half lines, 64 k, doubled the L2 requests)
-constexpr int kOutOfRange = 0x7FFFFFF0;  // past every range below: the load returns zeros
+constexpr int kOutOfRange = 1 << 30;  // past every range below (and no sum with it overflows): the load returns zeros
 constexpr int kCoherent = 0x10;          // sc1: agent-coherent, no cache maintenance needed
 constexpr int kMaxGroups = 512;          // persistent workgroups of a launch
 // A tile cut between workgroups has one arrival counter per wave, at zero
