@@ -36,20 +36,14 @@
 
 #include "layer_internal.h"
 #include "vq_device.h"
+#include "w8a8_plan.h"
 
 namespace vq {
 
 namespace {
 
-constexpr int KC = 128;  // k of a group's chunk: a 128-byte line of a row (half lines, 64 k, doubled the L2 requests)
 constexpr int kOutOfRange = 1 << 30;  // past every range below (and no sum with it overflows): the load returns zeros
 constexpr int kCoherent = 0x10;          // sc1: agent-coherent, no cache maintenance needed
-constexpr int kMaxGroups = 512;          // persistent workgroups of a launch
-// A tile cut between workgroups has one arrival counter per wave, at zero
-// between calls; the pieces begin where the verify GEMMs' do, so that a
-// workspace shared with them keeps their counters too.
-constexpr size_t kCounterBytes = 64 * 1024;
-static_assert(kMaxGroups * 8 * 4 <= kCounterBytes, "counters");
 constexpr int kStrip = 4;                // feature columns of tiles walked together
 
 struct KArgs {
@@ -509,81 +503,6 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     wait_vmcnt<0>();  // loads past the last chunk write LDS: none outlives the workgroup
 }
 
-// The forms of the kernel (template arguments and workgroups per CU) and what
-// each costs, in us: `begin` per launch, `tile` per tile of a workgroup (its
-// outputs), `join` + `piece` per piece where tiles are cut, and each round of
-// workgroups the longest of three: `chunk` per chunk, the bytes into LDS at
-// `l2` TB/s, its share of the weights at `hbm` TB/s, `again` of them for each
-// further row of tiles.  Fitted to 11,000 launches of 870 problems (1 to 4,093
-// rows, 128 to 17,408 features, k 256 to 17,408, plain and gated).  The form with
-// the least sum is launched: on those problems it took 2% more than the best one
-// in the mean and 1.4 times at worst (a 7 us launch); one form for each row
-// count took up to twice the best.
-struct Form {
-    int rt, ft, wr, wf, wk, stages, per_cu;
-    float begin, chunk, tile, join, piece, hbm, again, l2;
-    constexpr int rows() const { return 16 * rt * wr; }
-    constexpr int feats() const { return 16 * ft * wf; }
-};
-constexpr Form kForms[] = {
-    {1, 2, 1, 1, 4, 3, 2, 5.0f, 0.25f, 1.0f, 1.0f, 0.16f, 6.3f, 0.34f, 18.6f},  // 16 x 32
-    {1, 2, 1, 4, 1, 6, 1, 5.2f, 0.26f, 1.0f, 1.3f, 0.21f, 6.2f, 0.24f, 14.6f},  // 16 x 128
-    {2, 2, 1, 1, 4, 2, 2, 5.2f, 0.34f, 1.0f, 1.0f, 0.28f, 4.3f, 0.07f, 19.3f},  // 32 x 32
-    {4, 2, 1, 2, 2, 3, 1, 5.0f, 0.41f, 2.0f, 1.1f, 0.48f, 5.9f, 0.43f, 18.7f},  // 64 x 64
-    {4, 2, 1, 4, 1, 4, 1, 4.9f, 0.36f, 1.9f, 1.6f, 0.51f, 6.0f, 0.34f, 16.3f},  // 64 x 128
-    {4, 2, 2, 2, 1, 4, 1, 5.0f, 0.34f, 1.9f, 1.4f, 0.62f, 4.7f, 0.64f, 17.7f},  // 128 x 64
-    {4, 2, 2, 4, 1, 4, 1, 5.2f, 0.46f, 2.4f, 2.8f, 0.68f, 5.0f, 0.39f, 15.7f},  // 128 x 128
-    {8, 2, 2, 4, 1, 3, 1, 6.0f, 0.74f, 3.3f, 3.3f, 1.19f, 5.0f, 0.50f, 13.5f},  // 256 x 128
-    {8, 4, 2, 4, 1, 2, 1, 6.8f, 1.28f, 5.1f, 6.7f, 2.35f, 4.0f, 0.10f, 10.6f},  // 256 x 256
-};
-constexpr int kFormCount = sizeof(kForms) / sizeof(kForms[0]);
-
-// Forms whose tiles are at most half padding.
-bool fits_rows(const Form &f, int N) { return f.rows() == 16 || f.rows() < 2 * N; }
-
-int groups_of(const Form &f, int cus) { return std::min(cus * f.per_cu, kMaxGroups); }
-size_t pieces_bytes(const Form &f, int cus) {
-    return kCounterBytes + (size_t)groups_of(f, cus) * f.rows() * f.feats() * 4;
-}
-
-// How a launch cuts its tiles: `whole` of them by single workgroups, each of
-// the rest in `cuts` pieces.  Without room for the pieces every tile is whole.
-struct Plan {
-    int form, groups, whole, cuts;
-};
-
-Plan plan_of(const W8A8Args &p, bool gated, int cus) {
-    Plan best{};
-    float least = 0.f;
-    for (int i = 0; i < kFormCount; ++i) {
-        const Form &f = kForms[i];
-        if (!fits_rows(f, p.N))
-            continue;
-        const int G = groups_of(f, cus), feats = gated ? f.feats() / 2 : f.feats();
-        const int64_t rows = (p.N + f.rows() - 1) / f.rows(), cols = (p.M + feats - 1) / feats, tiles = rows * cols;
-        const int nch = (p.K + f.wk * KC - 1) / (f.wk * KC), rest = (int)(tiles % G);
-        const bool room = p.workspace && p.workspace_bytes >= pieces_bytes(f, cus);
-        const float weights = (float)p.M * (float)p.K * (gated ? 2.f : 1.f) * (1.f + f.again * (float)(rows - 1)) /
-                              (f.hbm * 1e6f * (float)tiles);  // us for a tile's share of them
-        const float chunk = (float)((f.rows() + f.feats()) * f.wk * KC) / (f.l2 * 1e6f);  // us for a chunk into LDS
-        const auto round = [&](int chunks, int groups, float tiles_in) {
-            return std::max({f.chunk * (float)chunks, chunk * (float)chunks * (float)groups, weights * tiles_in});
-        };
-        const float fixed = f.begin + f.tile * (float)((tiles + G - 1) / G) + (float)(tiles / G) * round(nch, G, (float)G);
-        const int most = rest && room ? std::min({G / rest, nch, 12}) : 1;
-        for (int cuts = 1; cuts <= most; ++cuts) {
-            const float us = fixed + (rest ? round((nch + cuts - 1) / cuts, rest * cuts, (float)rest) : 0.f) +
-                             (cuts == 1 ? 0.f : f.join + f.piece * (float)cuts);
-            if (best.groups == 0 || us < least) {
-                least = us;
-                best = cuts == 1 ? Plan{i, (int)std::min<int64_t>(tiles, G), (int)tiles, 0}
-                                 : Plan{i, tiles > G ? G : rest * cuts, (int)(tiles - rest), cuts};
-            }
-        }
-    }
-    return best;
-}
-
 int current_device() {
     int dev = 0;
     return hipGetDevice(&dev) == hipSuccess && dev >= 0 ? dev : 64;
@@ -654,7 +573,7 @@ hipError_t launch_rows(W8A8Args p) {
         part.x_scales += n0;
         part.out = static_cast<char *>(p.out) + (size_t)n0 * p.M * (p.out_dtype == VQ_DTYPE_F32 ? 4 : 2);
         part.N = std::min(most, N - n0);
-        const hipError_t e = launch_plan<GATED>(part, plan_of(part, GATED, cus), dev);
+        const hipError_t e = launch_plan<GATED>(part, plan_of(part.N, part.M, part.K, GATED, cus, part.workspace ? part.workspace_bytes : 0), dev);
         if (e != hipSuccess)
             return e;
     }

@@ -1,0 +1,45 @@
+"""How the 8-bit products are laid out, on the host: that every tile is
+computed once, that nothing is cut without room, and which forms the shapes of
+the GPU tests reach."""
+import random
+
+import pytest
+
+import plan_host as H
+import test_gpu_w8a8 as G
+
+SHAPES = [(n, m, k) for n in (1, 16, 17, 33, 100, 300, 4093) for m in (1, 130, 5120, 17408) for k in (16, 1040, 17408)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("cus", [256, 304, 80, 1])
+def test_every_tile_once(gated, cus):
+    """Whole tiles and cut ones together are the grid's tiles; the cut ones'
+    pieces are no more than the workgroups, which all of them run at once, nor
+    than the chunks."""
+    rng = random.Random(cus)
+    shapes = SHAPES + [(rng.randint(1, 5000), rng.randint(1, 20000), 16 * rng.randint(1, 1200)) for _ in range(300)]
+    for n, m, k in shapes:
+        for room in (0, H.ROOM):
+            p = H.plan(n, m, k, gated, room, cus)
+            rows, cols = H.tiles(p, n, m, gated)
+            rest = rows * cols - p.whole
+            assert 0 <= rest and p.groups >= 1, (n, m, k, p)
+            if room == 0 or rest == 0:
+                assert rest == 0 and p.cuts == 0, (n, m, k, p)
+            else:
+                assert p.cuts >= 2 and rest * p.cuts <= p.groups, (n, m, k, p)
+                assert p.cuts <= -(-k // (128 * p.wk)), (n, m, k, p)
+
+
+def test_the_gpu_shapes_reach_every_form():
+    """Each form with whole tiles, with cut tiles, and (for the large ones)
+    with whole rounds and cut tiles behind them."""
+    for shapes, gated in ((G.PLAIN, False), (G.GATED, True)):
+        seen = {}
+        for n, m, k in shapes:
+            p = H.plan(n, m, k, gated)
+            kind = "whole" if p.cuts == 0 else "cut" if p.whole == 0 else "both"
+            seen.setdefault(p.form, set()).add(kind)
+        assert sorted(seen) == list(range(H.lib().forms())), seen
+        assert all("whole" in kinds and len(kinds) > 1 for kinds in seen.values()), seen
