@@ -549,15 +549,8 @@ hipError_t launch_plan(const W8A8Args &p, const Plan &plan, int dev) {
     if constexpr (I + 1 < kFormCount)
         if (plan.form != I)
             return launch_plan<GATED, I + 1>(p, plan, dev);
-    // One row of tiles reads the weights once.  They are loaded past the caches
-    // where the 256 MB behind them could not keep them for the next call beside
-    // the rest of a layer (178 MB, 16 rows: 40.7 us, 43.3 with the caches), and
-    // through them where it could (42 MB, one row, three matrices in turn: 10.3
-    // us, 11.1 past them).
-    if constexpr (kForms[I].rows() == 16)
-        if ((int64_t)p.M * p.K * (GATED ? 2 : 1) >= (int64_t)128 << 20)
-            return launch_form<I, GATED, kAuxStream>(p, plan, dev);
-    return launch_form<I, GATED, kAuxCached>(p, plan, dev);
+    return past_caches(kForms[I], p.N, p.M, p.K, GATED) ? launch_form<I, GATED, kAuxStream>(p, plan, dev)
+                                                        : launch_form<I, GATED, kAuxCached>(p, plan, dev);
 }
 
 // Rows per launch: the tile numbers of a launch stay in 32 bits.

@@ -55,6 +55,26 @@ inline size_t pieces_bytes(const Form &f, int cus) {
     return kCounterBytes + (size_t)groups_of(f, cus) * f.rows() * f.feats() * 4;
 }
 
+// Whether a launch loads its weights past the caches.  Only where the 256 MB
+// behind them could not keep them for the next call beside the rest of a layer
+// (42 MB, one row, three matrices in turn: 11.1 us past them, 10.3 with), and
+// where no workgroup reads what another has read before:
+//  - One row of tiles reads each weight once: gated 17408 x 5120 (178 MB) of 16
+//    rows 39.9 us past the caches and 43.4 with, of 61 rows 38.8 and 43.0, of 256
+//    in 256 x 128 tiles 73.7 and 76.8.
+//  - More rows of tiles find them in L2 only while they keep together, and a last
+//    row of few rows, with less to load, runs ahead: 17 rows 17408 to 8192 in 16 x
+//    32 tiles 44.2 us past and 33.9 with, gated 65 rows in 64 x 128 tiles 63.1 and
+//    50.9, 129 rows in 128 x 64 tiles 107 and 74.
+//  - Two rows of 16 x 128 tiles do keep together, nine tenths of their loads being
+//    weights: gated 17 rows 41.6 and 45.7, 32 rows 42.6 and 47.6; three do not (48
+//    rows 70.5 and 67.1).
+inline bool past_caches(const Form &f, int N, int M, int K, bool gated) {
+    const int rows = (N + f.rows() - 1) / f.rows();
+    return (int64_t)M * K * (gated ? 2 : 1) >= (int64_t)128 << 20 &&
+           (rows == 1 || (rows == 2 && f.rows() == 16 && f.feats() == 128));
+}
+
 // How a launch cuts its tiles: `whole` of them by single workgroups, each of
 // the rest in `cuts` pieces.  Without room for the pieces every tile is whole.
 struct Plan {

@@ -16,15 +16,16 @@ _SOURCE = r"""
 extern "C" void plan(int n, int m, int k, int gated, int cus, size_t room, int *o) {
     const vq::Plan p = vq::plan_of(n, m, k, gated != 0, cus, room);
     const vq::Form &f = vq::kForms[p.form];
-    const int v[] = {p.form, p.groups, p.whole, p.cuts, f.rows(), f.feats(), f.wk};
-    for (int i = 0; i < 7; ++i)
+    const int v[] = {p.form, p.groups, p.whole, p.cuts, f.rows(), f.feats(), f.wk,
+                     vq::past_caches(f, n, m, k, gated != 0)};
+    for (int i = 0; i < 8; ++i)
         o[i] = v[i];
 }
 extern "C" int forms() { return vq::kFormCount; }
 extern "C" size_t counter_bytes() { return vq::kCounterBytes; }
 """
 
-Plan = collections.namedtuple("Plan", "form groups whole cuts rows feats wk")
+Plan = collections.namedtuple("Plan", "form groups whole cuts rows feats wk past")
 
 
 @functools.lru_cache(maxsize=None)
@@ -44,7 +45,7 @@ def lib():
 
 
 def plan(n, m, k, gated=False, room=ROOM, cus=CUS):
-    o = (ctypes.c_int * 7)()
+    o = (ctypes.c_int * 8)()
     lib().plan(n, m, k, gated, cus, room, o)
     return Plan(*o)
 

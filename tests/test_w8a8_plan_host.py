@@ -43,3 +43,21 @@ def test_the_gpu_shapes_reach_every_form():
             seen.setdefault(p.form, set()).add(kind)
         assert sorted(seen) == list(range(H.lib().forms())), seen
         assert all("whole" in kinds and len(kinds) > 1 for kinds in seen.values()), seen
+
+
+def test_weights_read_again_stay_in_the_caches():
+    """Weights are loaded past the caches only where they are too large for
+    them and are read by one row of tiles, or by two of 16 x 128, whatever the
+    height of the form: 17 to 32 rows in 16 x 32 tiles are two rows of them."""
+    big = [(17408, 17408), (8192, 17408), (17408, 8192), (40960, 4096), (5120, 65536)]
+    seen = set()
+    for gated in (False, True):
+        for m, k in big + [(5120, 8192), (700, 17408)]:
+            for n in (1, 9, 16, 17, 24, 32, 33, 40, 61, 64, 65, 100, 129, 256, 257, 2048):
+                p = H.plan(n, m, k, gated)
+                rows = H.tiles(p, n, m, gated)[0]
+                large = m * k * (2 if gated else 1) >= 128 << 20
+                assert p.past == (large and (rows == 1 or (rows == 2 and (p.rows, p.feats) == (16, 128)))), (n, m, k, p)
+                seen.add((large, min(rows, 3), p.rows, p.past))
+    assert {(True, 1, 16, 1), (True, 1, 64, 1), (True, 2, 16, 0), (True, 2, 16, 1), (False, 1, 16, 0)} <= seen, seen
+    assert not H.plan(17, 8192, 17408).past and H.plan(16, 8192, 17408).past and H.plan(61, 17408, 5120, True).past
