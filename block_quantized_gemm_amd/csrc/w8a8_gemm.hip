@@ -378,6 +378,7 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         asm volatile("" ::: "memory");
         // so many loads go out together, of kBatch workgroups' pieces or of a part of one
         constexpr int kTiles = FT * RT, kAtOnce = kTiles <= 16 ? kTiles : 8, kBatch = kTiles <= 8 ? 8 / kTiles : 1;
+        static_assert(kTiles % kAtOnce == 0, "every tile of a wave is in a batch");
         for (int w0 = 0; w0 < a.cuts; w0 += kBatch) {
             static_for<kTiles / kAtOnce>([&](auto H) {
                 u32x4 v[kBatch][kAtOnce];
