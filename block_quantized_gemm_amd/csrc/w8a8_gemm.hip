@@ -65,21 +65,40 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 // The activations are written so that no large term is subtracted from
 // another: 0.5 g (1 + tanh z) = g / (1 + exp(-2 z)), and the Gaussian's
 // distribution function as 0.5 erfc(-g / sqrt 2).  exp and the quotient are the
-// hardware's base-2 power and reciprocal (one unit each, two roundings beside
-// them): the product's rounding of g, three of them, moves the result by more.
-// An accurate exp and division took 11 us of a 256 x 128 tile, these 2.
+// hardware's base-2 power and reciprocal, one unit each.
+//
+// For 16-bit outputs the exponent t is formed in fp32: its two to five
+// roundings, |t| ln 2 times as large relative to the result, stay below 2^-15 of
+// it (|t| <= 126, beyond which it is 0), a sixteenth of what the output's
+// rounding may move it.
 __device__ __forceinline__ float over_one_plus_exp2(float g, float t) {  // g / (1 + 2^t)
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }
-__device__ __forceinline__ float activate(float g, int kind) {
-    constexpr float kLog2e = 1.4426950408889634f;
-    if (kind == VQ_ACT_SILU)
-        return over_one_plus_exp2(g, -kLog2e * g);
-    if (kind == VQ_ACT_GELU_TANH) {
-        constexpr float kA = -2.0f * kLog2e * 0.7978845608028654f, kB = kA * 0.044715f;
-        return over_one_plus_exp2(g, g * __builtin_fmaf(kB * g, g, kA));
+// For fp32 outputs t is formed and reduced in 64 bits, the power is of a
+// fraction of at most one half, and a step on the reciprocal leaves it rounded:
+// within 7 half units in all, subnormal results too (the other way up to 28 for
+// SiLU and 73 for the tanh form, where g is negative).  2,048 rows gated take 341
+// us this way and 328 the other; the exact GELU's erfcf 361.
+__device__ __forceinline__ float over_one_plus_exp2(float g, double t) {
+    const double m = fmin(fabs(t), 300.0), n = rint(m);
+    const float e = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(n - m)), -(int)n);  // 2^-|t|
+    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+    return g * (t > 0 ? e : 1.0f) * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+template <int KIND, typename T>  // T: what t is formed in
+__device__ __forceinline__ float activate(float g) {
+    if constexpr (KIND == VQ_ACT_GELU) {
+        return 0.5f * g * erfcf(g * -0.7071067811865476f);
+    } else {
+        constexpr double kLog2e = 1.4426950408889634, kRoot = 0.7978845608028654;  // sqrt(2 / pi)
+        const T x = g;
+        if constexpr (KIND == VQ_ACT_SILU) {
+            return over_one_plus_exp2(g, (T)-kLog2e * x);
+        } else {
+            constexpr T kA = -2 * kLog2e * kRoot, kB = -2 * kLog2e * kRoot * 0.044715;
+            return over_one_plus_exp2(g, x * __builtin_elementwise_fma(kB * x, x, kA));
+        }
     }
-    return 0.5f * g * erfcf(g * -0.7071067811865476f);
 }
 
 // A wave's 16-byte LDS read takes four cycles of 16 lanes, the first two {0-3,
@@ -257,7 +276,7 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         const int f0 = fb + wf * FO * 16;
         if constexpr (GATED) {
             const rsrc_t rsu = make_rsrc(a.up_scales, (uint32_t)a.M * 4u);
-            const auto all = [&](auto KIND) {
+            const auto all = [&](auto KIND, auto T) {
 #pragma unroll
                 for (int ft = 0; ft < FO; ++ft)
 #pragma unroll
@@ -267,18 +286,21 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
                         const float su = __builtin_bit_cast(float, bload4<kAuxCached>(rsu, o, 0));
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
-                            const float gate = activate((float)acc[ft][rt][r] * sx[rt] * sg, KIND.value);
+                            const float gate = activate<KIND.value, decltype(T)>((float)acc[ft][rt][r] * sx[rt] * sg);
                             acc[ft][rt][r] =
                                 __builtin_bit_cast(int, gate * ((float)acc[ft + FO][rt][r] * sx[rt] * su));
                         }
                     }
             };
-            if (a.activation == VQ_ACT_SILU)
-                all(std::integral_constant<int, VQ_ACT_SILU>{});
-            else if (a.activation == VQ_ACT_GELU)
-                all(std::integral_constant<int, VQ_ACT_GELU>{});
+            using Silu = std::integral_constant<int, VQ_ACT_SILU>;
+            using Tanh = std::integral_constant<int, VQ_ACT_GELU_TANH>;
+            const bool fine = a.out_dtype == VQ_DTYPE_F32;
+            if (a.activation == VQ_ACT_GELU)
+                all(std::integral_constant<int, VQ_ACT_GELU>{}, 0.f);
+            else if (a.activation == VQ_ACT_SILU)
+                fine ? all(Silu{}, 0.0) : all(Silu{}, 0.f);
             else
-                all(std::integral_constant<int, VQ_ACT_GELU_TANH>{});
+                fine ? all(Tanh{}, 0.0) : all(Tanh{}, 0.f);
         } else {
             const bool biased = a.bias != nullptr;
             const rsrc_t rb4 = make_rsrc(biased ? a.bias : a.w_scales, (uint32_t)a.M * 4u);

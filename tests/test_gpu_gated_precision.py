@@ -1,0 +1,57 @@
+"""The gated product's activations in fp32 outputs, where the factors are exact:
+one nonzero code a row and channel and scales that are powers of two, so that
+what is off is the activation's own."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_gemm_amd as vq
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _gated(scale, act, rows, out=torch.float32):
+    """(g, act(g)) for g = a c scale, all codes a of the rows and c of the channels."""
+    a, c = np.resize(np.arange(-127, 128), rows), np.arange(-127, 128)
+    x, wg, wu = (np.zeros((n, 16), np.int8) for n in (rows, len(c), len(c)))
+    x[:, 0], x[:, 1], wg[:, 0], wu[:, 1] = a, 1, c, 1
+    one = torch.ones(max(rows, len(c)), device="cuda")
+    got = vq.gated_w8a8(torch.from_numpy(wg).cuda(), scale * one[:len(c)], torch.from_numpy(wu).cuda(), one[:len(c)],
+                        torch.from_numpy(x).cuda(), one[:rows], torch.empty(rows, len(c), device="cuda", dtype=out),
+                        activation=act)
+    return (a[:, None] * c).astype(np.float64) * scale, got.double().cpu().numpy()
+
+
+def _exact(g, act):
+    t = g if act == "silu" else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+    with np.errstate(over="ignore"):
+        return np.where(t > 0, g / (1 + np.exp(-np.abs(t))), g * np.exp(-np.abs(t)) / (1 + np.exp(-np.abs(t))))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("scale", [2.0 ** -16, 2.0 ** -13, 2.0 ** -11, 2.0 ** -9, 2.0 ** -7])
+@pytest.mark.parametrize("rows", [5, 255, 600])
+def test_fp32_outputs(act, scale, rows):
+    """In half units U of fp32: the power 2 and 0.2 (its argument's rounding,
+    2^-26 ln 2), the sum 1, the reciprocal 1.1 after its step (the square of its
+    own unit is below 0.1), two products 1 each: 6.3.  Below the normal numbers
+    the power and the result are rounded to 2^-150."""
+    g, got = _gated(scale, act, rows)
+    want = _exact(g, act)
+    off = np.abs(got - want) / (7 * U * np.abs(want) + (np.abs(g) + 1) * 2.0 ** -150 + 1e-300)
+    assert off.max() <= 1.0, (off.max(), g.flat[off.argmax()])
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_16_bit_outputs(act, out):
+    """The output's rounding, the exponent's (2^-15 of the result) and the rest
+    (7 U); results below 2^-126 |g| may be 0."""
+    for scale in (2.0 ** -13, 2.0 ** -9, 2.0 ** -7):
+        g, got = _gated(scale, act, 300, out)
+        want = _exact(g, act)
+        fi = torch.finfo(out)
+        bound = (fi.eps / 2 + 1.01 * 2.0 ** -15 + 7 * U) * np.abs(want) + fi.smallest_normal * fi.eps / 2 + \
+            2.0 ** -126 * (np.abs(g) + 1)
+        assert (np.abs(got - want) <= bound).all()
