@@ -180,6 +180,32 @@ __global__ __launch_bounds__(1024) void row_norm_kernel(KArgs a) {
         if (gated_rows)
             rg[i] = load8<false>(a.gate, row + at[i]);
     }
+    // 1 / sqrt(mean(v^2) + eps).  Where that mean is below 2^-90 or infinite, so
+    // that squares may have left fp32's range, v is multiplied by a power of two
+    // first and stays so: v times the result is what it would be.
+    const auto inverse_rms = [&](float (&v)[VPT][8]) {
+        const auto mean = [&] {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (in[i])
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum = __builtin_fmaf(v[i][e], v[i][e], sum);
+            return reduce(sum, lds, sum_of) / (float)a.C;
+        };
+        float m = mean() + a.eps;
+        if (!(m >= 0x1p-90f && m <= 3.4028235e38f)) {  // (the same bits in every thread)
+            const float s = m < 1.0f ? 0x1p100f : 0x1p-100f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] *= s;
+            m = mean() + a.eps * s * s;
+        }
+        return 1.0f / sqrtf(m);
+    };
     float x[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -189,17 +215,7 @@ __global__ __launch_bounds__(1024) void row_norm_kernel(KArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             to_float<false>(ry[i], y_bf, y[i]);
-        float inv = 1.0f;
-        if (a.post_weight) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (in[i])
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum = __builtin_fmaf(y[i][e], y[i][e], sum);
-            inv = 1.0f / sqrtf(reduce(sum, lds, sum_of) / (float)a.C + a.eps);
-        }
+        const float inv = a.post_weight ? inverse_rms(y) : 1.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float t[8];
@@ -225,14 +241,7 @@ __global__ __launch_bounds__(1024) void row_norm_kernel(KArgs a) {
                 store8(a.residual_out, a.residual_dtype, row + at[i], x[i]);
         }
     }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        if (in[i])
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum = __builtin_fmaf(x[i][e], x[i][e], sum);
-    const float inv = 1.0f / sqrtf(reduce(sum, lds, sum_of) / (float)a.C + a.eps);
+    const float inv = inverse_rms(x);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float t[8];

@@ -688,8 +688,8 @@ int vq_gated_w8a8(const int8_t *w_gate, const float *gate_scales, const int8_t *
  *   h = x / sqrt(mean(x^2) + eps) * weight   (weight NULL: 1)
  *   out = h rounded to out_dtype F16 or BF16, or for I8 the codes and scale of
  *         vq_quant_rows_int8 for the row h
- * All of it fp32, from x before its rounding; a row's sum of squares must stay
- * below the fp32 maximum.
+ * All of it fp32, from x before its rounding; rows whose squares leave fp32's
+ * range are normed like any other.
  *   residual  [N][C], residual_dtype F16, BF16 or F32; residual_out may be
  *             residual (in place)
  *   y         [N][C], y_dtype F16 or BF16, or NULL (then post_weight, gate and
