@@ -10,6 +10,7 @@ contiguity, and pass raw pointers plus the current torch stream to the library.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -183,17 +184,44 @@ def _check_2d(t, name, shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
+@contextlib.contextmanager
+def _outside_captures(dev):
+    """A stream of `dev`, current meanwhile, on which nothing is captured: work
+    issued here runs now, also while this thread captures a graph.  (A thread's
+    usual mode ends its captures when it allocates memory.)"""
+    torch = _torch()
+    mode, exchange = ctypes.c_int(_CAPTURE_RELAXED), None
+    if torch.cuda.is_initialized():
+        exchange = ctypes.CDLL(LIB_PATH).hipThreadExchangeStreamCaptureMode  # of the runtime that libvq is linked to
+        exchange(ctypes.byref(mode))
+    try:
+        if not torch.cuda.is_current_stream_capturing():
+            yield torch.cuda.current_stream(dev)
+            return
+        for _ in range(64):  # torch hands out its streams in turn, the captured one among them
+            stream = torch.cuda.Stream(dev)
+            with torch.cuda.stream(stream):
+                if not torch.cuda.is_current_stream_capturing():
+                    yield stream
+                    return
+        raise RuntimeError("every stream is being captured")
+    finally:
+        if exchange is not None:
+            exchange(ctypes.byref(mode))
+
+
 class Workspace:
     """A zero-filled device buffer for the walk form of the verify GEMMs:
     arrival counters and the partial sums of tile groups cut between two
     workgroups.
 
     The library leaves the counters at zero after every call, so it is zeroed
-    once.  The zero fill runs on torch's current stream and is waited for here,
-    so the buffer is ready for a call on any stream.  Calls sharing one
-    workspace must be ordered (one stream, or streams the caller orders), and
-    so must the replays of a graph captured with it (with "auto": the buffer of
-    the stream that the graph was captured on).  The calls of several kernels
+    once.  The zero fill is waited for here, so the buffer is ready for a call on
+    any stream; it is never part of a graph, also when this thread is capturing
+    one.  Calls sharing one workspace must be ordered (one stream, or streams
+    the caller orders), and so must the replays of graphs captured with it (with
+    "auto": the buffer of the stream that a graph was captured on, so graphs
+    whose replays overlap are captured on streams of their own).  The calls of several kernels
     that pass data through the buffer (greedy and tree verification, tree
     attention) hold `lock` while they enqueue them, so that host threads which
     share a workspace on one stream do not interleave."""
@@ -201,9 +229,8 @@ class Workspace:
     def __init__(self, nbytes: int, device=None):
         torch = _torch()
         dev = torch.device(device if device is not None else "cuda")
-        alloc = torch.cuda.current_stream(dev)
-        self.tensor = torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
-        if not torch.cuda.is_current_stream_capturing():
+        with _outside_captures(dev) as alloc:
+            self.tensor = torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
             alloc.synchronize()
         self._streams = {alloc.cuda_stream}
         self.lock = threading.Lock()
@@ -224,6 +251,8 @@ class Workspace:
             self.tensor.record_stream(torch.cuda.ExternalStream(stream_handle, device=self.tensor.device))
             self._streams.add(stream_handle)
 
+
+_CAPTURE_RELAXED = 2  # hipStreamCaptureModeRelaxed
 
 _auto_ws = {}
 _outgrown_ws = []
@@ -995,10 +1024,7 @@ class _Args:
 
 
 def _product_workspace(n, workspace, device, stream_handle):
-    """(pointer, bytes) for a product of 8-bit codes with n rows.  A cached
-    workspace is not made while a graph is captured: its zero fill would run with
-    the graph's replays only, and eager calls share it.  The captured call then
-    runs without one (the same bits)."""
+    """(pointer, bytes) for a product of 8-bit codes with n rows."""
     if workspace is None:
         return None, 0
     query = "vq_w8a8_workspace_bytes"
@@ -1008,8 +1034,6 @@ def _product_workspace(n, workspace, device, stream_handle):
             need = _ws_needs[(query, n)] = w8a8_workspace_bytes(n)
         ws = _auto_ws.get((query, device, stream_handle))
         if ws is None or ws.nbytes < need:
-            if _torch().cuda.is_current_stream_capturing():
-                return None, 0
             ws = _auto_workspace((query, device, stream_handle), need, device)
     elif isinstance(workspace, Workspace):
         ws = workspace
@@ -1026,8 +1050,8 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     [N], as quant_rows_int8 and residual_norm write them; bias: float32 [M] or
     None; out: float16 / bfloat16 / float32 [N][M].  The integer sums are exact:
     a row's bits do not depend on the other rows.  workspace: "auto" (a cached
-    one per device and stream; while a graph is captured, only one that an
-    earlier call made), a Workspace, or None (a slower form, the same bits)."""
+    one per device and stream, which graphs captured on that stream share), a
+    Workspace, or None (a slower form, the same bits)."""
     torch = _torch()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N][K] and w [M][K]")
