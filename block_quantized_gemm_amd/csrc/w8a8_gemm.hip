@@ -65,39 +65,36 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 // The activations are written so that no large term is subtracted from
 // another: 0.5 g (1 + tanh z) = g / (1 + exp(-2 z)), and the Gaussian's
 // distribution function as 0.5 erfc(-g / sqrt 2).  exp and the quotient are the
-// hardware's base-2 power and reciprocal, one unit each.
-//
-// For 16-bit outputs the exponent t is formed in fp32: its two to five
-// roundings, |t| ln 2 times as large relative to the result, stay below 2^-15 of
-// it (|t| <= 126, beyond which it is 0), a sixteenth of what the output's
-// rounding may move it.
+// hardware's base-2 power and reciprocal, one unit each.  The power's exponent t
+// is fp32: its roundings, two for SiLU and five for the tanh form, are |t| ln 2
+// times as large relative to the result.  For 16-bit outputs that is below 2^-15
+// (|t| <= 126, beyond which the result is 0), a sixteenth of what their own
+// rounding may move it; for fp32 outputs the tanh form has no fewer in the plain
+// order of its formula, but SiLU has: there (FINE) the power is corrected by what
+// the exponent's roundings took, which leaves it within 8 half units instead of
+// 28 (g = -15): 2,048 rows gated to fp32 347 us, 336 without.
 __device__ __forceinline__ float over_one_plus_exp2(float g, float t) {  // g / (1 + 2^t)
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }
-// For fp32 outputs t is formed and reduced in 64 bits, the power is of a
-// fraction of at most one half, and a step on the reciprocal leaves it rounded:
-// within 7 half units in all, subnormal results too (the other way up to 28 for
-// SiLU and 73 for the tanh form, where g is negative).  2,048 rows gated take 341
-// us this way and 328 the other; the exact GELU's erfcf 361.
-__device__ __forceinline__ float over_one_plus_exp2(float g, double t) {
-    const double m = fmin(fabs(t), 300.0), n = rint(m);
-    const float e = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(n - m)), -(int)n);  // 2^-|t|
-    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
-    return g * (t > 0 ? e : 1.0f) * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-}
-template <int KIND, typename T>  // T: what t is formed in
+template <int KIND, bool FINE>
 __device__ __forceinline__ float activate(float g) {
-    if constexpr (KIND == VQ_ACT_GELU) {
-        return 0.5f * g * erfcf(g * -0.7071067811865476f);
+    constexpr float kLog2e = 1.4426950408889634f;
+    if constexpr (KIND == VQ_ACT_SILU && FINE) {
+        // |x| log2 e < 128: the power stays finite, and where it passes 2^126 its
+        // reciprocal is 0
+        constexpr float kMost = 88.72f, kLn2 = 0.6931471805599453f;
+        constexpr float kLow = (float)(1.4426950408889634 - (double)kLog2e);
+        const float x = __builtin_amdgcn_fmed3f(g, -kMost, kMost), t = -kLog2e * x;
+        const float lost = __builtin_fmaf(-kLow, x, __builtin_fmaf(-kLog2e, x, -t));
+        const float e = __builtin_amdgcn_exp2f(t);
+        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, lost * kLn2, e));
+    } else if constexpr (KIND == VQ_ACT_SILU) {
+        return over_one_plus_exp2(g, -kLog2e * g);
+    } else if constexpr (KIND == VQ_ACT_GELU_TANH) {
+        constexpr float kA = -2.0f * kLog2e * 0.7978845608028654f, kB = kA * 0.044715f;
+        return over_one_plus_exp2(g, g * __builtin_fmaf(kB * g, g, kA));
     } else {
-        constexpr double kLog2e = 1.4426950408889634, kRoot = 0.7978845608028654;  // sqrt(2 / pi)
-        const T x = g;
-        if constexpr (KIND == VQ_ACT_SILU) {
-            return over_one_plus_exp2(g, (T)-kLog2e * x);
-        } else {
-            constexpr T kA = -2 * kLog2e * kRoot, kB = -2 * kLog2e * kRoot * 0.044715;
-            return over_one_plus_exp2(g, x * __builtin_elementwise_fma(kB * x, x, kA));
-        }
+        return 0.5f * g * erfcf(g * -0.7071067811865476f);
     }
 }
 
@@ -130,8 +127,10 @@ struct Part {
 // RT x FT tiles of 16 rows x 16 features per wave, WR x WF waves that share
 // their operands, and WK such groups that share a tile's k: a chunk is WK
 // times KC = 128 k, group i's the i-th 128, in STAGES stages.
+// FINE: gated to fp32 (kernels of their own: one more epilogue beside the others
+// slowed those, 2,048 rows to 16 bits from 319 to 327 us).
 // AUX: the cache policy of the weights' loads.
-template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED, int AUX>
+template <int RT, int FT, int WR, int WF, int WK, int STAGES, bool GATED, bool FINE, int AUX>
 __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
     constexpr int kWaves = WR * WF, BM = 16 * RT * WR, BF = 16 * FT * WF;
     constexpr int kWPieces = BF / 8, kXPieces = BM / 8;  // 1 KiB each, a wave's load: 8 rows of KC bytes
@@ -276,7 +275,7 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
         const int f0 = fb + wf * FO * 16;
         if constexpr (GATED) {
             const rsrc_t rsu = make_rsrc(a.up_scales, (uint32_t)a.M * 4u);
-            const auto all = [&](auto KIND, auto T) {
+            const auto all = [&](auto KIND) {
 #pragma unroll
                 for (int ft = 0; ft < FO; ++ft)
 #pragma unroll
@@ -286,21 +285,18 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
                         const float su = __builtin_bit_cast(float, bload4<kAuxCached>(rsu, o, 0));
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
-                            const float gate = activate<KIND.value, decltype(T)>((float)acc[ft][rt][r] * sx[rt] * sg);
+                            const float gate = activate<KIND.value, FINE>((float)acc[ft][rt][r] * sx[rt] * sg);
                             acc[ft][rt][r] =
                                 __builtin_bit_cast(int, gate * ((float)acc[ft + FO][rt][r] * sx[rt] * su));
                         }
                     }
             };
-            using Silu = std::integral_constant<int, VQ_ACT_SILU>;
-            using Tanh = std::integral_constant<int, VQ_ACT_GELU_TANH>;
-            const bool fine = a.out_dtype == VQ_DTYPE_F32;
-            if (a.activation == VQ_ACT_GELU)
-                all(std::integral_constant<int, VQ_ACT_GELU>{}, 0.f);
-            else if (a.activation == VQ_ACT_SILU)
-                fine ? all(Silu{}, 0.0) : all(Silu{}, 0.f);
+            if (a.activation == VQ_ACT_SILU)
+                all(std::integral_constant<int, VQ_ACT_SILU>{});
+            else if (a.activation == VQ_ACT_GELU)
+                all(std::integral_constant<int, VQ_ACT_GELU>{});
             else
-                fine ? all(Tanh{}, 0.0) : all(Tanh{}, 0.f);
+                all(std::integral_constant<int, VQ_ACT_GELU_TANH>{});
         } else {
             const bool biased = a.bias != nullptr;
             const rsrc_t rb4 = make_rsrc(biased ? a.bias : a.w_scales, (uint32_t)a.M * 4u);
@@ -364,7 +360,7 @@ __global__ __launch_bounds__(64 * WR * WF * WK) void w8a8_kernel(KArgs a) {
                 }
             }
         };
-        if (a.out_dtype == VQ_DTYPE_F32)
+        if (FINE || (!GATED && a.out_dtype == VQ_DTYPE_F32))
             all(std::integral_constant<int, VQ_DTYPE_F32>{});
         else if (a.out_dtype == VQ_DTYPE_BF16)
             all(std::integral_constant<int, VQ_DTYPE_BF16>{});
@@ -544,13 +540,13 @@ int device_cus(int dev) {
     return n;
 }
 
-template <int I, bool GATED, int AUX>
+template <int I, bool GATED, bool FINE, int AUX>
 hipError_t launch_form(const W8A8Args &p, const Plan &plan, int dev) {
     constexpr Form f = kForms[I];
     constexpr int BM = f.rows(), BF = f.feats(), kOutFeats = GATED ? BF / 2 : BF;
     constexpr int kLds = f.wk * f.stages * (BF + BM) * KC + (f.wk - 1) * BM * BF * 4;
     static_assert(kLds * f.per_cu <= 160 * 1024, "LDS");
-    const auto kern = w8a8_kernel<f.rt, f.ft, f.wr, f.wf, f.wk, f.stages, GATED, AUX>;
+    const auto kern = w8a8_kernel<f.rt, f.ft, f.wr, f.wf, f.wk, f.stages, GATED, FINE, AUX>;
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much LDS
     if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
@@ -572,8 +568,13 @@ hipError_t launch_plan(const W8A8Args &p, const Plan &plan, int dev) {
     if constexpr (I + 1 < kFormCount)
         if (plan.form != I)
             return launch_plan<GATED, I + 1>(p, plan, dev);
-    return past_caches(kForms[I], p.N, p.M, p.K, GATED) ? launch_form<I, GATED, kAuxStream>(p, plan, dev)
-                                                        : launch_form<I, GATED, kAuxCached>(p, plan, dev);
+    const bool past = past_caches(kForms[I], p.N, p.M, p.K, GATED);
+    if constexpr (GATED)
+        if (p.out_dtype == VQ_DTYPE_F32)
+            return past ? launch_form<I, true, true, kAuxStream>(p, plan, dev)
+                        : launch_form<I, true, true, kAuxCached>(p, plan, dev);
+    return past ? launch_form<I, GATED, false, kAuxStream>(p, plan, dev)
+                : launch_form<I, GATED, false, kAuxCached>(p, plan, dev);
 }
 
 // Rows per launch: the tile numbers of a launch stay in 32 bits.

@@ -669,10 +669,11 @@ int vq_gemm_w8a8(const int8_t *w, const float *w_scales, const int8_t *x, const 
  * products of vq_gemm_w8a8 (no bias) with w_gate and w_up, [F][K] each: both
  * projections of a gated feed-forward block, its activation and the product in
  * one pass over the weights; g and u are not stored.  g, u, act and their
- * product are fp32, rounded once.  For F32 outputs SiLU and the tanh GELU of an
- * fp32 g are within 7 * 2^-24 of their value; for 16-bit outputs within 2^-15,
- * and 0 where they are below 2^-126 |g|.  w_gate and w_up may be the halves of one
- * [2 F][K] matrix.  Same sizes (F in place of M) and reproducibility.
+ * product are fp32, rounded once.  For F32 outputs SiLU is within 8 * 2^-24 of
+ * its value for the fp32 g, the tanh GELU within the roundings of its fp32
+ * argument z, (7 + 16 |z|) * 2^-24; for 16-bit outputs both are within 2^-15 and
+ * the output's rounding.  Where they are below 2^-126 |g| they may be 0.
+ * w_gate and w_up may be the halves of one [2 F][K] matrix.  Same sizes (F in place of M) and reproducibility.
  * Returns VQ_ERR_BAD_CONFIG for an unknown activation.
  */
 int vq_gated_w8a8(const int8_t *w_gate, const float *gate_scales, const int8_t *w_up, const float *up_scales,
