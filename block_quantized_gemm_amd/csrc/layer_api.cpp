@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -102,7 +103,7 @@ int vq_residual_norm(const void *residual, int residual_dtype, const void *y, in
         return VQ_ERR_BAD_SHAPE;
     if (!y && (post_weight || gate || residual_out))  // there is no update to apply them to
         return VQ_ERR_BAD_CONFIG;
-    if (!(eps >= 0.0f) || eps > 3.0e38f)
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
         return VQ_ERR_BAD_CONFIG;
     if (!aligned({residual, y, post_weight, gate, weight, residual_out, out}, 16) || !aligned({scales_out}, 4))
         return VQ_ERR_MISALIGNED;
