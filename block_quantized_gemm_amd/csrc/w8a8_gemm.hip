@@ -24,14 +24,19 @@
 //
 // Nine forms, chosen by their estimated time (kForms).  For few rows, groups of
 // waves split a tile's k and each streams for itself, without barriers: 1 row
-// 8192 to 5120 in 10 us (4.2 TB/s), 16 rows 5120 to 17408 in 20.5 us (4.4 TB/s, a
-// copy reaches 4.9), 16 rows gated 17408 in 41 us; bound by the weights' bytes
-// and 5 us of launch, first loads and last stores.  For many, 256 x 256 tiles:
-// 4,093 rows 17408 to 5120 in 294 us (2,479 TOPS), 4,096 rows to 8192 in 437 us
-// (2,670; the library int8 product of 8192^3 2,458), gated 2,048 rows in 316 us.
-// There the matrix instructions run 65% of the time: without the loads the loop
-// takes 328 of 437 us, with loads that all hit L2 392, without LDS reads either
-// 293.
+// 8192 to 5120 in 9.1 to 9.7 us (4.3 to 4.6 TB/s), 16 rows 5120 to 17408 in 19.3 to
+// 20.9 us (4.3 to 4.7 TB/s, a copy reaches 4.9), gated 16 rows 17408 in 40 us, 61
+// rows in 38; bound by the weights' bytes and 5 us of launch, first loads and last
+// stores.  For many, 256 x 256 tiles: 4,093 rows 17408 to 5120 in 294 to 302 us
+// (2,416 to 2,480 TOPS; the library int8 product of 8192^3 2,458), 4,096 rows to
+// 8192 in 432 to 461, gated 2,048 rows in 316 to 321.  There the matrix
+// instructions run 60% (4,093 rows) and 70% (4,096) of the time.  With parts left
+// out, before the loads were spread between them, the loop of the 4,096 rows took
+// 328 of then 437 us without the loads, 392 with loads that all hit L2, 293
+// without LDS reads either.  Between the two, 64 to 1,000 rows take 1.4 to 2.3
+// times their floor: tiles of 128 and 256 rows pad, and 128 x 128 ones bring a
+// third more bytes into LDS than 256 x 128 (300 rows 17408 to 5120 44 us, floor
+// 21.8).
 #include <atomic>
 
 #include "layer_internal.h"
@@ -72,7 +77,7 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 // rounding may move it; for fp32 outputs the tanh form has no fewer in the plain
 // order of its formula, but SiLU has: there (FINE) the power is corrected by what
 // the exponent's roundings took, which leaves it within 8 half units instead of
-// 28 (g = -15): 2,048 rows gated to fp32 347 us, 336 without.
+// 28 (g down to -31): 2,048 rows gated to fp32 347 us, 336 without.
 __device__ __forceinline__ float over_one_plus_exp2(float g, float t) {  // g / (1 + 2^t)
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }

@@ -23,11 +23,13 @@ static_assert(kMaxGroups * 8 * 4 <= kCounterBytes, "counters");
 // outputs), `join` + `piece` per piece where tiles are cut, and each round of
 // workgroups the longest of three: `chunk` per chunk, the bytes into LDS at
 // `l2` TB/s, its share of the weights at `hbm` TB/s, `again` of them for each
-// further row of tiles.  Fitted to 11,000 launches of 870 problems (1 to 4,093
-// rows, 128 to 17,408 features, k 256 to 17,408, plain and gated).  The form with
-// the least sum is launched: on those problems it took 2% more than the best one
-// in the mean and 1.4 times at worst (a 7 us launch); one form for each row
-// count took up to twice the best.
+// further row of tiles.  Fitted to 11,000 launches of 870 problems, before the
+// loads were spread between the matrix instructions and the weights' cache policy
+// was what it is.  The form with the least sum is launched.  On the kernel as it
+// is, over 928 problems (1 to 4,093 rows, 128 to 17,408 features, k 256 to 17,408,
+// plain and gated; 17,600 launches of every form and cut), that took 1.7% more than
+// the best one in the mean and 1.34 times at worst (24 rows 17408 to 5120, 30.8 us
+// for 23.0); one form for each row count had taken up to twice the best.
 struct Form {
     int rt, ft, wr, wf, wk, stages, per_cu;
     float begin, chunk, tile, join, piece, hbm, again, l2;
