@@ -94,6 +94,7 @@ SIGNATURES = {
     "vq_gemm_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
     "vq_gated_w8a8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I64, _I64, _I64, _P, _SZ, _P]),
     "vq_w8a8_workspace_bytes": (_SZ, [_I64]),
+    "vq_w8a8_workspace_used": (_SZ, [_I64, _I64, _I64, _I]),
     "vq_residual_norm": (_I, [_P, _I, _P, _I, _P, _P, _I, _F, _P, _F, _P, _P, _I, _P, _I64, _I64, _P]),
     "vq_quant_rows_int8": (_I, [_P, _I, _P, _P, _I64, _I64, _P]),
     "vq_rotate": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I,
@@ -184,17 +185,49 @@ def _check_2d(t, name, shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
+_hip_functions = {}
+
+
+def _hip(name, *argtypes):
+    """A function of the HIP runtime that libvq is linked to."""
+    fn = _hip_functions.get(name)
+    if fn is None:
+        fn = getattr(ctypes.CDLL(LIB_PATH), name)
+        fn.argtypes, fn.restype = argtypes, _I
+        _hip_functions[name] = fn
+    return fn
+
+
+@contextlib.contextmanager
+def _relaxed_captures():
+    """Lets this thread allocate and wait while it captures a graph (in a
+    thread's usual mode that ends its captures)."""
+    if not _torch().cuda.is_initialized():
+        yield
+        return
+    mode, exchange = _I(_CAPTURE_RELAXED), _hip("hipThreadExchangeStreamCaptureMode", ctypes.POINTER(_I))
+    exchange(ctypes.byref(mode))
+    try:
+        yield
+    finally:
+        exchange(ctypes.byref(mode))
+
+
+def _capture_id(stream_handle: int) -> int:
+    """Which capture is going on on a stream; 0: none."""
+    status, which = _I(0), ctypes.c_ulonglong(0)
+    info = _hip("hipStreamGetCaptureInfo", _P, ctypes.POINTER(_I), ctypes.POINTER(ctypes.c_ulonglong))
+    if info(stream_handle, ctypes.byref(status), ctypes.byref(which)) != 0 or status.value != _CAPTURE_ACTIVE:
+        return 0
+    return which.value
+
+
 @contextlib.contextmanager
 def _outside_captures(dev):
     """A stream of `dev`, current meanwhile, on which nothing is captured: work
-    issued here runs now, also while this thread captures a graph.  (A thread's
-    usual mode ends its captures when it allocates memory.)"""
+    issued here runs now, also while this thread captures a graph."""
     torch = _torch()
-    mode, exchange = ctypes.c_int(_CAPTURE_RELAXED), None
-    if torch.cuda.is_initialized():
-        exchange = ctypes.CDLL(LIB_PATH).hipThreadExchangeStreamCaptureMode  # of the runtime that libvq is linked to
-        exchange(ctypes.byref(mode))
-    try:
+    with _relaxed_captures():
         if not torch.cuda.is_current_stream_capturing():
             yield torch.cuda.current_stream(dev)
             return
@@ -205,9 +238,6 @@ def _outside_captures(dev):
                     yield stream
                     return
         raise RuntimeError("every stream is being captured")
-    finally:
-        if exchange is not None:
-            exchange(ctypes.byref(mode))
 
 
 class Workspace:
@@ -252,7 +282,7 @@ class Workspace:
             self._streams.add(stream_handle)
 
 
-_CAPTURE_RELAXED = 2  # hipStreamCaptureModeRelaxed
+_CAPTURE_RELAXED, _CAPTURE_ACTIVE = 2, 1  # hipStreamCaptureModeRelaxed, hipStreamCaptureStatusActive
 
 _auto_ws = {}
 _outgrown_ws = []
@@ -1023,8 +1053,8 @@ class _Args:
                     raise ValueError("%s must not share memory with %s" % (name, other))
 
 
-def _product_workspace(n, workspace, device, stream_handle):
-    """(pointer, bytes) for a product of 8-bit codes with n rows."""
+def _product_workspace(n, m, k, gated, workspace, device, stream_handle):
+    """(pointer, bytes) for a product of 8-bit codes."""
     if workspace is None:
         return None, 0
     query = "vq_w8a8_workspace_bytes"
@@ -1034,6 +1064,11 @@ def _product_workspace(n, workspace, device, stream_handle):
             need = _ws_needs[(query, n)] = w8a8_workspace_bytes(n)
         ws = _auto_ws.get((query, device, stream_handle))
         if ws is None or ws.nbytes < need:
+            capture = _capture_id(stream_handle)
+            if capture:
+                if w8a8_workspace_used(n, m, k, gated) == 0:
+                    return None, 0
+                return _graph_workspace(capture, need, device, stream_handle)
             ws = _auto_workspace((query, device, stream_handle), need, device)
     elif isinstance(workspace, Workspace):
         ws = workspace
@@ -1043,6 +1078,33 @@ def _product_workspace(n, workspace, device, stream_handle):
     return ws.ptr(), ws.nbytes
 
 
+_COUNTER_BYTES = 64 * 1024  # of a workspace, in front of the pieces: zero between calls
+_graph_ws = {}
+
+
+def _graph_workspace(capture: int, need: int, device, stream_handle: int):
+    """(pointer, bytes) of a workspace that the products of one stream share
+    within one capture: memory of the graph, whose counters the graph clears
+    itself, so that no other graph and no eager call uses it.  The reference is
+    kept until the stream's next capture, so that the graph's other tensors are
+    not laid over it; the memory lives as long as the graph.  Without (None, 0)
+    where the capture is not torch's, which has no such memory."""
+    torch = _torch()
+    key = (device, stream_handle)
+    held = _graph_ws.get(key)
+    if held is None or held[0] != capture or held[1].numel() < need:
+        stream = torch.cuda.ExternalStream(stream_handle, device=device)
+        with _relaxed_captures(), torch.cuda.stream(stream):
+            t = torch.empty(need, dtype=torch.uint8, device=device)
+            at = t.data_ptr()
+            if not any(tuple(seg["segment_pool_id"]) != (0, 0) for seg in torch.cuda.memory_snapshot()
+                       if seg["address"] <= at < seg["address"] + seg["total_size"]):
+                return None, 0
+            t[:_COUNTER_BYTES].zero_()
+        held = _graph_ws[key] = (capture, t)
+    return held[1].data_ptr(), held[1].numel()
+
+
 def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", stream=None):
     """out[N][M] = x_scales[n] * w_scales[m] * (x[N][K] @ w[M][K]^T) + bias[m].
 
@@ -1050,8 +1112,9 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     [N], as quant_rows_int8 and residual_norm write them; bias: float32 [M] or
     None; out: float16 / bfloat16 / float32 [N][M].  The integer sums are exact:
     a row's bits do not depend on the other rows.  workspace: "auto" (a cached
-    one per device and stream, which graphs captured on that stream share), a
-    Workspace, or None (a slower form, the same bits)."""
+    one per device and stream; under capture, one that an earlier call on the
+    stream made, shared with it, else one of the graph's own), a Workspace, or
+    None (a slower form, the same bits)."""
     torch = _torch()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [N][K] and w [M][K]")
@@ -1065,7 +1128,7 @@ def gemm_w8a8(w, w_scales, x, x_scales, out, *, bias=None, workspace="auto", str
     po = a.array(out, "out", (N, M), out.dtype)
     a.apart(1)
     sh = _raw_stream(stream)
-    wp, wn = _product_workspace(N, workspace, x.device, sh)
+    wp, wn = _product_workspace(N, M, K, False, workspace, x.device, sh)
     st = lib().vq_gemm_w8a8(pw, pws, px, pxs, pb, po, _dtype_code(out), N, M, K, wp, wn, sh)
     _check(st, "vq_gemm_w8a8")
     return out
@@ -1094,11 +1157,17 @@ def gated_w8a8(w_gate, gate_scales, w_up, up_scales, x, x_scales, out, *, activa
     po = a.array(out, "out", (N, F), out.dtype)
     a.apart(1)
     sh = _raw_stream(stream)
-    wp, wn = _product_workspace(N, workspace, x.device, sh)
+    wp, wn = _product_workspace(N, F, K, True, workspace, x.device, sh)
     st = lib().vq_gated_w8a8(pg, pgs, pu, pus, px, pxs, ACTIVATIONS[activation], po, _dtype_code(out), N, F, K, wp, wn,
                              sh)
     _check(st, "vq_gated_w8a8")
     return out
+
+
+def w8a8_workspace_used(n_rows: int, m: int, k: int, gated: bool = False) -> int:
+    """Bytes that gemm_w8a8 (or gated_w8a8, m its F) writes of a workspace of
+    w8a8_workspace_bytes(n_rows): 0 where its tiles are not cut."""
+    return int(lib().vq_w8a8_workspace_used(n_rows, m, k, gated))
 
 
 def w8a8_workspace_bytes(n_rows: int) -> int:

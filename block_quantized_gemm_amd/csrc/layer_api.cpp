@@ -68,6 +68,12 @@ size_t vq_w8a8_workspace_bytes(int64_t n_rows) {
     return in(n_rows, 1, VQ_MAX_DIM) ? vq::w8a8_workspace((int)n_rows) : 0;
 }
 
+size_t vq_w8a8_workspace_used(int64_t n_rows, int64_t m, int64_t k, int gated) {
+    return in(n_rows, 1, VQ_MAX_DIM) && product_ok(m, k)
+               ? vq::w8a8_workspace_used((int)n_rows, (int)m, (int)k, gated != 0)
+               : 0;
+}
+
 int vq_gemm_w8a8(const int8_t *w, const float *w_scales, const int8_t *x, const float *x_scales, const float *bias,
                  void *out, int out_dtype, int64_t n_rows, int64_t m, int64_t k, void *workspace,
                  size_t workspace_bytes, void *stream) {

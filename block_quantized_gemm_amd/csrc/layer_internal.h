@@ -30,6 +30,7 @@ struct W8A8Args {
 };
 hipError_t launch_w8a8(const W8A8Args &a);
 size_t w8a8_workspace(int N);  // for N rows of any product
+size_t w8a8_workspace_used(int N, int M, int K, bool gated);  // of that
 
 // Arguments of one residual update with its norms, already checked.
 struct RowNormArgs {

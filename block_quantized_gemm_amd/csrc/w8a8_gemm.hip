@@ -582,12 +582,10 @@ hipError_t launch_plan(const W8A8Args &p, const Plan &plan, int dev) {
                 : launch_form<I, GATED, false, kAuxCached>(p, plan, dev);
 }
 
-// Rows per launch: the tile numbers of a launch stay in 32 bits.
 template <bool GATED>
 hipError_t launch_rows(W8A8Args p) {
     const int dev = current_device(), cus = device_cus(dev);
-    const int64_t cols = (p.M + 15) / 16;
-    const int most = (int)std::min<int64_t>(VQ_MAX_DIM, std::max<int64_t>(256, ((int64_t)1 << 30) / cols / 16 * 256));
+    const int most = rows_at_once(p.N, p.M);
     const int N = p.N;
     for (int n0 = 0; n0 < N; n0 += most) {
         W8A8Args part = p;
@@ -611,6 +609,16 @@ size_t w8a8_workspace(int N) {
         if (fits_rows(f, N))
             need = std::max(need, pieces_bytes(f, cus));
     return need;
+}
+
+size_t w8a8_workspace_used(int N, int M, int K, bool gated) {
+    const int cus = device_cus(current_device()), most = rows_at_once(N, M);
+    const size_t room = w8a8_workspace(N);
+    size_t used = 0;
+    for (int n : {most, N % most})  // the launches' sizes
+        if (n > 0)
+            used = std::max(used, plan_bytes(plan_of(n, M, K, gated, cus, room), n, M, gated));
+    return used;
 }
 
 hipError_t launch_w8a8(const W8A8Args &p) { return p.up ? launch_rows<true>(p) : launch_rows<false>(p); }

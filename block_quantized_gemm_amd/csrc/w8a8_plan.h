@@ -116,4 +116,20 @@ inline Plan plan_of(int N, int M, int K, bool gated, int cus, size_t room) {
     return best;
 }
 
+// Rows per launch: the tile numbers of a launch stay in 32 bits.
+inline int rows_at_once(int N, int M) {
+    const int64_t cols = (M + 15) / 16;
+    return (int)std::min<int64_t>(N, std::max<int64_t>(256, ((int64_t)1 << 30) / cols / 16 * 256));
+}
+
+// Bytes that a launch writes of a workspace with room for every form.
+inline size_t plan_bytes(const Plan &p, int N, int M, bool gated) {
+    if (p.cuts == 0)
+        return 0;
+    const Form &f = kForms[p.form];
+    const int feats = gated ? f.feats() / 2 : f.feats();
+    const int64_t tiles = (int64_t)((N + f.rows() - 1) / f.rows()) * ((M + feats - 1) / feats);
+    return kCounterBytes + (size_t)(tiles - p.whole) * p.cuts * f.rows() * f.feats() * 4;
+}
+
 }  // namespace vq

@@ -759,6 +759,12 @@ int vq_rotate(const void *q, int64_t q_stride, const void *k, int64_t k_stride, 
  * (greedy and tree verification, tree attention). */
 size_t vq_w8a8_workspace_bytes(int64_t n_rows);
 
+/* Bytes that a product of these sizes (gated != 0: vq_gated_w8a8, m its F)
+ * writes of a workspace of vq_w8a8_workspace_bytes(n_rows): 0 where its tiles
+ * are not cut, so that it runs the same form without one (and for sizes
+ * outside the limits). */
+size_t vq_w8a8_workspace_used(int64_t n_rows, int64_t m, int64_t k, int gated);
+
 /*
  * vq_hbm_read_probe -- a plain read of `bytes` of device memory at `buf`,
  * the bandwidth the verify GEMM's weight stream is measured against ([P1]

@@ -1,6 +1,9 @@
-"""Default workspaces that are made while a graph is captured: zeroed once, now,
-and not by the graph's replays; the capture goes on; calls before, between and
-after the replays are right."""
+"""Default workspaces that are first needed while a graph is captured: the
+8-bit products get one of the graph's own, the verify GEMMs the stream's, zeroed
+outside the graph; the capture goes on; calls before, between and after the
+replays are right."""
+import ctypes
+
 import pytest
 import torch
 
@@ -57,9 +60,125 @@ def _of(stream):
     return [ws for key, ws in vq._auto_ws.items() if key[-1] == stream.cuda_stream]
 
 
-@pytest.mark.parametrize("make,n,m,k", CALLS)
-def test_first_call_is_captured(make, n, m, k):
+def _graph_workspace(stream):
+    return vq._graph_ws[(torch.device("cuda", 0), stream.cuda_stream)][1]
+
+
+@pytest.mark.parametrize("make,n,m,k", CALLS[:4])
+def test_first_product_is_captured(make, n, m, k):
     call, out = make(n, m, k)
+    want = call().clone()
+    s = _fresh_stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call()
+        call()
+        other = torch.full((1 << 22,), 5, dtype=torch.int32, device="cuda")  # the graph's, not over the workspace
+    assert not _of(s)  # eager calls have none of it
+    buffer = _graph_workspace(s)
+    counters = buffer[:H.lib().counter_bytes()]
+    for i in range(4):
+        out.fill_(-1)
+        counters.fill_(0xFF)  # whatever ended in between: the graph clears them
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and not counters.any() and buffer.any() and (other == 5).all(), i
+        out.fill_(-1)
+        with torch.cuda.stream(s):
+            call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and not counters.any(), i
+    assert len(_of(s)) == 1 and _of(s)[0].ptr() != buffer.data_ptr()
+
+
+def test_a_product_that_is_not_cut_needs_none():
+    w, ws, x, xs = _codes(1, 5120, 1024, 3)
+    assert vq.w8a8_workspace_used(1, 5120, 1024) == 0
+    out = torch.empty(1, 5120, device="cuda")
+    want = vq.gemm_w8a8(w, ws, x, xs, out).clone()
+    s = _fresh_stream()
+    torch.cuda.synchronize()
+    graph, before = torch.cuda.CUDAGraph(), dict(vq._graph_ws)
+    with torch.cuda.graph(graph, stream=s):
+        vq.gemm_w8a8(w, ws, x, xs, out)
+    assert vq._graph_ws == before and not _of(s)
+    out.fill_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_graphs_of_one_stream_overlap():
+    """Captured one after the other on one stream, as torch does by default,
+    without a call before; the second needs more. Replayed at once on two streams,
+    also after the second capture has let go of the first one's buffer."""
+    made = [make(n, m, k) for make, n, m, k in (CALLS[3], CALLS[0], CALLS[1])]
+    want = [call().clone() for call, _ in made]
+    s, graphs = _fresh_stream(), []
+    for call, out in made:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(20):
+                call()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        for _, out in made:
+            out.fill_(-1)
+        filled = [torch.full((1 << 20,), 0x3C, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        for t, g in zip(streams, graphs):
+            with torch.cuda.stream(t):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, w) for (_, out), w in zip(made, want))
+        assert all(bool((f == 0x3C).all()) for f in filled)
+
+
+def test_a_larger_call_in_one_capture():
+    (small, a), (large, b) = _plain(98, 2633, 6240), _plain(227, 2101, 4176)
+    want = small().clone(), large().clone()
+    s = _fresh_stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        small(), large(), small()
+    for _ in range(4):
+        a.fill_(-1), b.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_capture_that_is_not_of_torch():
+    """Through the runtime itself: no memory of a graph's own, so no workspace."""
+    call, out = _plain(98, 2633, 6240)
+    want = call().clone()
+    s = _fresh_stream()
+    torch.cuda.synchronize()
+    P, pp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)
+    graph, made = P(), P()
+    assert vq._hip("hipStreamBeginCapture", P, ctypes.c_int)(s.cuda_stream, 0) == 0
+    try:
+        call(stream=s)
+    finally:
+        assert vq._hip("hipStreamEndCapture", P, pp)(s.cuda_stream, ctypes.byref(graph)) == 0
+    assert (torch.device("cuda", 0), s.cuda_stream) not in vq._graph_ws and not _of(s)
+    assert vq._hip("hipGraphInstantiate", pp, P, P, P, ctypes.c_size_t)(ctypes.byref(made), graph, None, None, 0) == 0
+    for _ in range(3):
+        out.fill_(-1)
+        torch.cuda.synchronize()
+        assert vq._hip("hipGraphLaunch", P, P)(made, s.cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert vq._hip("hipGraphExecDestroy", P)(made) == 0 and vq._hip("hipGraphDestroy", P)(graph) == 0
+
+
+def test_first_verify_gemm_is_captured():
+    call, out = _q4_0(4, 4096, 5120)
     want = call().clone()
     s = _fresh_stream()
     torch.cuda.synchronize()
@@ -68,28 +187,20 @@ def test_first_call_is_captured(make, n, m, k):
         call()
     ws, = _of(s)
     assert not ws.tensor.any(), "zeroed when it was made"
+    counters = ws.tensor[:H.lib().counter_bytes()]
     with torch.cuda.stream(s):  # before any replay
         out.fill_(-1)
         call()
     torch.cuda.synchronize()
-    assert torch.equal(out, want)
-    used, counters = ws.tensor.any().item(), ws.tensor[:H.lib().counter_bytes()]
-    assert used and not counters.any()
-    mark = make is not _q4_0  # (their workspaces hold more than these forms use)
+    assert torch.equal(out, want) and ws.tensor.any() and not counters.any()
     for _ in range(4):
-        out.fill_(-1)
-        if mark:
-            ws.tensor[-1] = 77
-        torch.cuda.synchronize()
-        graph.replay()
-        torch.cuda.synchronize()
-        assert torch.equal(out, want) and not counters.any()
-        assert not mark or ws.tensor[-1] == 77, "a replay clears the workspace"
-        out.fill_(-1)
-        with torch.cuda.stream(s):
-            call()
-        torch.cuda.synchronize()
-        assert torch.equal(out, want)
+        for run in (graph.replay, call):
+            out.fill_(-1)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(s):
+                run()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and not counters.any()
 
 
 @pytest.mark.parametrize("make,n,m,k", CALLS)
@@ -113,29 +224,3 @@ def test_captured_stream_that_is_not_current(make, n, m, k):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
-
-
-def test_graphs_of_two_streams_overlap():
-    """Captured on streams of their own, without a call before: each has its workspace."""
-    made = [make(n, m, k) for make, n, m, k in CALLS[:2]]
-    want = [call().clone() for call, _ in made]
-    streams, graphs = [], []
-    for call, out in made:
-        s = _fresh_stream()
-        torch.cuda.synchronize()
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g, stream=s):
-            for _ in range(20):
-                call()
-        streams.append(s)
-        graphs.append(g)
-    assert _of(streams[0])[0].ptr() != _of(streams[1])[0].ptr()
-    for _ in range(5):
-        for _, out in made:
-            out.fill_(-1)
-        torch.cuda.synchronize()
-        for s, g in zip(streams, graphs):
-            with torch.cuda.stream(s):
-                g.replay()
-        torch.cuda.synchronize()
-        assert all(torch.equal(out, w) for (_, out), w in zip(made, want))

@@ -5,6 +5,7 @@ import random
 
 import pytest
 
+import block_quantized_gemm_amd as vq
 import plan_host as H
 import test_gpu_w8a8 as G
 
@@ -61,3 +62,17 @@ def test_weights_read_again_stay_in_the_caches():
                 seen.add((large, min(rows, 3), p.rows, p.past))
     assert {(True, 1, 16, 1), (True, 1, 64, 1), (True, 2, 16, 0), (True, 2, 16, 1), (False, 1, 16, 0)} <= seen, seen
     assert not H.plan(17, 8192, 17408).past and H.plan(16, 8192, 17408).past and H.plan(61, 17408, 5120, True).past
+
+
+def test_bytes_used_of_a_workspace():
+    """As the library answers (it takes 256 compute units where there is no
+    device): 0 exactly where nothing is cut, never more than what is asked for."""
+    for gated in (False, True):
+        for n, m, k in SHAPES + (G.GATED if gated else G.PLAIN):
+            used, p = vq.w8a8_workspace_used(n, m, k, gated), H.plan(n, m, k, gated)
+            rows, cols = H.tiles(p, n, m, gated)
+            pieces = (rows * cols - p.whole) * p.cuts * p.rows * p.feats * 4
+            assert used == (H.lib().counter_bytes() + pieces if p.cuts else 0), (n, m, k, p)
+            assert used <= vq.w8a8_workspace_bytes(n)
+    for bad in ((0, 16, 16), (1, 0, 16), (1, 16, 24), (1, 16, 0), ((1 << 24) + 1, 16, 16), (1, 16, 131072)):
+        assert vq.w8a8_workspace_used(*bad) == 0
