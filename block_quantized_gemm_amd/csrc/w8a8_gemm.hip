@@ -29,7 +29,7 @@
 // rows in 38; bound by the weights' bytes and 5 us of launch, first loads and last
 // stores.  For many, 256 x 256 tiles: 4,093 rows 17408 to 5120 in 294 to 302 us
 // (2,416 to 2,480 TOPS; the library int8 product of 8192^3 2,458), 4,096 rows to
-// 8192 in 432 to 461, gated 2,048 rows in 316 to 321.  There the matrix
+// 8192 in 432 to 461, gated 2,048 rows in 316 to 322.  There the matrix
 // instructions run 60% (4,093 rows) and 70% (4,096) of the time.  With parts left
 // out, before the loads were spread between them, the loop of the 4,096 rows took
 // 328 of then 437 us without the loads, 392 with loads that all hit L2, 293
